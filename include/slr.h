@@ -388,6 +388,51 @@ SLR_API slr_status slr_forward_ex(const void *X, int64_t M, const void *vals, co
                                   int64_t d_in, const void *U, const void *V, int64_t r, void *Y, void *workspace,
                                   size_t workspace_bytes, slr_path path, uint32_t flags, slr_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Forward pass with bias, activation and residual in its epilogue.
+ *
+ *        Z = X * S^T + (X * V^T) * U^T + b        Y = act(Z) + R
+ *
+ * The layer of LoSparse section 3.2 as a network uses it (its pages replace
+ * the linear layers of encoders whose MLPs have biases and a GELU); one call
+ * instead of the product followed by passes over Y.  The kernels are those of
+ * slr_forward: the epilogue works on the fp32 accumulators before their one
+ * rounding to bf16.
+ *
+ *   X ... r, Y, workspace, path, flags  as slr_forward_ex.
+ *   bias  device, bf16 [d_out], or NULL (no bias).
+ *   act   the activation.  GELU is z * Phi(z); GELU_TANH the tanh form
+ *         z * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; SILU
+ *         z / (1 + exp(-z)).  NaN stays NaN.
+ *   R     device, bf16 [M, ldr] (ldr >= d_out), or NULL (no residual; ldr is
+ *         then not looked at).  R may be Y itself (same pointer, ldr ==
+ *         d_out): the residual stream is then updated in place.  Otherwise R
+ *         must not overlap an output.
+ *   Z     device, bf16 [M, d_out], out, or NULL: the pre-activation, rounded to
+ *         bf16, for slr_epilogue_backward.
+ *
+ * With SLR_FWD_OVERLAP_PRECEDING, bias counts as a weight (the preceding
+ * kernel must not write it); R is read after the preceding kernel is done.
+ * Without bias, activation, residual and Z the result is slr_forward_ex's, bit
+ * for bit.
+ *
+ * Accuracy: Z as slr_forward's product; the activation is evaluated in fp32.
+ * Requirements: those of slr_forward_ex; bias and R may have any alignment
+ * that their type has (2 bytes), Z the same.
+ * ------------------------------------------------------------------------ */
+typedef enum slr_act {
+    SLR_ACT_NONE = 0,
+    SLR_ACT_RELU = 1,
+    SLR_ACT_GELU = 2,
+    SLR_ACT_GELU_TANH = 3,
+    SLR_ACT_SILU = 4
+} slr_act;
+
+SLR_API slr_status slr_forward_epilogue(const void *X, int64_t M, const void *vals, const void *meta, int64_t d_out,
+                                        int64_t d_in, const void *U, const void *V, int64_t r, const void *bias,
+                                        slr_act act, const void *R, int64_t ldr, void *Z, void *Y, void *workspace,
+                                        size_t workspace_bytes, slr_path path, uint32_t flags, slr_stream_t stream);
+
 /* The two stages of slr_forward, for callers that schedule or time them
  * separately.  slr_forward(...) == slr_forward_project(...) followed on the same
  * stream by slr_forward_combine(...) with the same path and workspace.

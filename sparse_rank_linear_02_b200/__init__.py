@@ -17,6 +17,8 @@ Functions mirror the C ABI in ``include/slr.h``:
   ``slr_decompose_datafree``
 * ``forward(X, vals, meta, U, V) -> Y``  -- ``slr_forward`` /
   ``slr_forward_with_path`` / ``slr_forward_ex``
+* ``forward_epilogue(X, vals, meta, U, V, bias, act, residual) -> Y``  --
+  ``slr_forward_epilogue``
 * ``workspace_size``, ``select_path``, ``check_kernel_error``
 
 Tensors are torch CUDA tensors (torch only provides memory and the current
@@ -38,6 +40,7 @@ STATUS_NAMES = {0: "SLR_OK", 1: "SLR_ERR_NULL", 2: "SLR_ERR_SHAPE", 3: "SLR_ERR_
                 7: "SLR_ERR_TIMEOUT", 8: "SLR_ERR_ARG"}
 PATHS = {"auto": 0, "decode": 1, "tensor": 2}
 PATH_NAMES = {v: k for k, v in PATHS.items()}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class SlrError(RuntimeError):
@@ -87,6 +90,9 @@ def _load() -> ctypes.CDLL:
     lib.slr_forward_with_path.argtypes = [p, i64, p, p, i64, i64, p, p, i64, p, p, sz, st, p]
     lib.slr_forward_ex.restype = st
     lib.slr_forward_ex.argtypes = [p, i64, p, p, i64, i64, p, p, i64, p, p, sz, st, ctypes.c_uint32, p]
+    lib.slr_forward_epilogue.restype = st
+    lib.slr_forward_epilogue.argtypes = [p, i64, p, p, i64, i64, p, p, i64, p, st, p, i64, p, p, p, sz, st,
+                                         ctypes.c_uint32, p]
     lib.slr_forward_workspace_size.restype = sz
     lib.slr_forward_workspace_size.argtypes = [i64, i64, i64, i64]
     lib.slr_forward_select_path.restype = st
@@ -138,6 +144,46 @@ def _ptr(t: torch.Tensor | None):
 def _check(status: int, what: str):
     if status != SLR_OK:
         raise SlrError(status, what)
+
+
+def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, like: torch.Tensor):
+    """Refuse an operand whose type, shape, layout or device is not what the call reads."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}, not "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _expect_current(t: torch.Tensor):
+    """The kernels run on the current device's current stream, where the operands have to be."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the operands are on {t.device}, not on the current CUDA device")
+
+
+def _expect_layer(vals: torch.Tensor, meta: torch.Tensor, U: torch.Tensor | None, V: torch.Tensor | None,
+                  like: torch.Tensor) -> tuple[int, int, int]:
+    """(d_out, d_in, r) of a packed layer, its operands checked."""
+    if vals.dim() != 2 or (U is None) != (V is None):
+        raise ValueError("vals must be 2-D, and U and V come together")
+    d_out, d_in = vals.shape[0], 2 * vals.shape[1]
+    _expect("vals", vals, torch.bfloat16, (d_out, d_in // 2), like)
+    _expect("meta", meta, torch.uint8, (d_out, meta_row_bytes(d_in)), like)
+    if U is None:
+        return d_out, d_in, 0
+    r = V.shape[0]
+    _expect("U", U, torch.bfloat16, (d_out, r), like)
+    _expect("V", V, torch.bfloat16, (r, d_in), like)
+    return d_out, d_in, r
+
+
+def _scratch(workspace: torch.Tensor | None, need: int, like: torch.Tensor) -> tuple[torch.Tensor | None, int]:
+    """The caller's workspace, or a new one where the call needs it, and its bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif not workspace.is_contiguous() or workspace.device != like.device:
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def meta_row_bytes(d_in: int) -> int:
@@ -325,6 +371,49 @@ def forward(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, U: torch.Te
     _check(_lib.slr_forward_ex(_ptr(X), M, _ptr(vals), _ptr(meta), d_out, d_in, _ptr(U), _ptr(V), r,
                                _ptr(out), _ptr(workspace), ws_bytes, PATHS[path], flags, _stream()),
            "slr_forward")
+    return out
+
+
+def forward_epilogue(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, U: torch.Tensor | None,
+                     V: torch.Tensor | None, *, bias: torch.Tensor | None = None, act: str = "none",
+                     residual: torch.Tensor | None = None, preact: torch.Tensor | None = None, path: str = "auto",
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     overlap_preceding: bool = False) -> torch.Tensor:
+    """``Y = act(X @ S.T + (X @ V.T) @ U.T + bias) + residual`` in the kernels of
+    :func:`forward` (``slr_forward_epilogue``).
+
+    ``bias`` is bf16 [d_out], ``act`` one of :data:`ACTS`, ``residual`` bf16
+    [M, d_out] with unit column stride (its rows may be a slice of wider ones;
+    ``out`` itself updates it in place).  ``preact`` (bf16 [M, d_out]) receives
+    the pre-activation for :func:`epilogue_backward`.  The workspace is
+    :func:`forward`'s (:func:`workspace_size`)."""
+    if X.dim() != 2 or act not in ACTS:
+        raise ValueError(f"X must be 2-D and act one of {', '.join(ACTS)}")
+    _expect_current(X)
+    M = X.shape[0]
+    d_out, d_in, r = _expect_layer(vals, meta, U, V, X)
+    _expect("X", X, torch.bfloat16, (M, d_in), X)
+    if out is None:
+        out = torch.empty((M, d_out), dtype=torch.bfloat16, device=X.device)
+    else:
+        _expect("out", out, torch.bfloat16, (M, d_out), X)
+    if bias is not None:
+        _expect("bias", bias, torch.bfloat16, (d_out,), X)
+    if preact is not None:
+        _expect("preact", preact, torch.bfloat16, (M, d_out), X)
+    ldr = d_out
+    if residual is not None:
+        if residual.dtype != torch.bfloat16 or residual.shape != (M, d_out) or residual.device != X.device or \
+                (d_out > 1 and residual.stride(1) != 1):
+            raise ValueError(f"residual must be a bf16 tensor of shape {(M, d_out)} on {X.device} with unit column "
+                             f"stride")
+        if M > 1:
+            ldr = residual.stride(0)
+    ws, ws_bytes = _scratch(workspace, workspace_size(M, d_out, d_in, r), X)
+    flags = FWD_OVERLAP_PRECEDING if overlap_preceding else 0
+    _check(_lib.slr_forward_epilogue(_ptr(X), M, _ptr(vals), _ptr(meta), d_out, d_in, _ptr(U), _ptr(V), r, _ptr(bias),
+                                     ACTS[act], _ptr(residual), ldr, _ptr(preact), _ptr(out), _ptr(ws), ws_bytes,
+                                     PATHS[path], flags, _stream()), "slr_forward_epilogue")
     return out
 
 

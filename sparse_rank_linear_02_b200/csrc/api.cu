@@ -3,6 +3,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "tc_forward.cuh"
 
 namespace slr {
@@ -17,6 +18,10 @@ constexpr double kSmallProjectXBytes = 12.0 * 1024 * 1024;
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+bool act_ok(int act) { return act >= SLR_ACT_NONE && act <= SLR_ACT_SILU; }
 
 // sm_100 check, cached per device ordinal.
 slr_status check_device() {
@@ -127,7 +132,7 @@ cudaError_t run_project(const void *X, int64_t M, const void *V, int64_t d_in, i
 // launch, 1 right after the projection, 2 chained.
 cudaError_t run_combine(const void *X, int64_t M, const void *vals, const void *meta, int64_t d_out, int64_t d_in,
                         const void *U, int64_t r, void *Y, const void *workspace, slr_path p, int pdl,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, const Epilogue *ep = nullptr) {
     const uint16_t *x = static_cast<const uint16_t *>(X);
     const uint16_t *v = static_cast<const uint16_t *>(vals);
     const uint8_t *m = static_cast<const uint8_t *>(meta);
@@ -135,9 +140,9 @@ cudaError_t run_combine(const void *X, int64_t M, const void *vals, const void *
     uint16_t *y = static_cast<uint16_t *>(Y);
     if (p == SLR_PATH_DECODE)
         return launch_decode_forward(x, M, v, m, d_out, d_in, u, r > 0 ? static_cast<const float *>(workspace) : nullptr,
-                                     r, y, pdl, stream);
+                                     r, y, pdl, stream, ep);
     return launch_tc_forward(x, M, v, m, d_out, d_in, u, r > 0 ? static_cast<const uint16_t *>(workspace) : nullptr,
-                             r, y, pdl, stream);
+                             r, y, pdl, stream, ep);
 }
 
 // Whether a call with SLR_FWD_OVERLAP_PRECEDING runs chained: the small-M
@@ -159,7 +164,8 @@ bool chain_supported(slr_path p, int64_t M, int64_t d_in, int64_t r) {
 // only before reading T.
 slr_status forward_impl(const void *X, int64_t M, const void *vals, const void *meta, int64_t d_out,
                         int64_t d_in, const void *U, const void *V, int64_t r, void *Y, void *workspace,
-                        size_t workspace_bytes, slr_path path, uint32_t flags, cudaStream_t stream) {
+                        size_t workspace_bytes, slr_path path, uint32_t flags, cudaStream_t stream,
+                        const Epilogue *ep = nullptr) {
     slr_path p;
     if ((flags & ~(uint32_t)SLR_FWD_OVERLAP_PRECEDING) != 0) return SLR_ERR_ARG;
     const slr_status st = validate(X, M, vals, meta, d_out, d_in, U, V, r, Y, workspace, workspace_bytes, path,
@@ -174,12 +180,12 @@ slr_status forward_impl(const void *X, int64_t M, const void *vals, const void *
                                       static_cast<const uint8_t *>(meta), d_out, d_in,
                                       static_cast<const uint16_t *>(U), static_cast<const uint16_t *>(V), r,
                                       static_cast<uint16_t *>(Y), static_cast<uint8_t *>(workspace), workspace_bytes,
-                                      stream);
+                                      stream, ep);
         return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
     }
     err = run_project(X, M, V, d_in, r, workspace, p, chained, stream);
     if (err == cudaSuccess)
-        err = run_combine(X, M, vals, meta, d_out, d_in, U, r, Y, workspace, p, chained ? 2 : 1, stream);
+        err = run_combine(X, M, vals, meta, d_out, d_in, U, r, Y, workspace, p, chained ? 2 : 1, stream, ep);
     return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
 }
 
@@ -473,6 +479,24 @@ slr_status slr_forward_ex(const void *X, int64_t M, const void *vals, const void
                           slr_path path, uint32_t flags, slr_stream_t stream) {
     return slr::forward_impl(X, M, vals, meta, d_out, d_in, U, V, r, Y, workspace, workspace_bytes, path, flags,
                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+slr_status slr_forward_epilogue(const void *X, int64_t M, const void *vals, const void *meta, int64_t d_out,
+                                int64_t d_in, const void *U, const void *V, int64_t r, const void *bias, slr_act act,
+                                const void *R, int64_t ldr, void *Z, void *Y, void *workspace, size_t workspace_bytes,
+                                slr_path path, uint32_t flags, slr_stream_t stream) {
+    if (!slr::act_ok(act)) return SLR_ERR_ARG;
+    if (R != nullptr && (ldr < d_out || (R == Y && ldr != d_out))) return SLR_ERR_SHAPE;
+    if (!slr::aligned2(bias) || !slr::aligned2(R) || !slr::aligned2(Z)) return SLR_ERR_ALIGN;
+    slr::Epilogue ep;
+    ep.bias = static_cast<const uint16_t *>(bias);
+    ep.res = static_cast<const uint16_t *>(R);
+    ep.ldr = ldr;
+    ep.pre = static_cast<uint16_t *>(Z);
+    ep.act = (int32_t)act;
+    const bool plain = bias == nullptr && R == nullptr && Z == nullptr && act == SLR_ACT_NONE;
+    return slr::forward_impl(X, M, vals, meta, d_out, d_in, U, V, r, Y, workspace, workspace_bytes, path, flags,
+                             reinterpret_cast<cudaStream_t>(stream), plain ? nullptr : &ep);
 }
 
 }  // extern "C"

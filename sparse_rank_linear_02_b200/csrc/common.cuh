@@ -54,6 +54,8 @@ __device__ __forceinline__ uint4 ld_dep_v4(const void *p) {
     return v;
 }
 
+struct Epilogue;   // epilogue.cuh
+
 // ---------------------------------------------------------------- launchers
 // Each returns cudaSuccess or the launch error; arguments were validated by
 // the API layer.
@@ -139,13 +141,13 @@ cudaError_t launch_lowrank_project(const uint16_t *X, int64_t M, const uint16_t 
 // pdl_mode: 0 = ordinary launch; 1 = the projection kernel that writes T32 is
 // the kernel launched immediately before on `stream` (programmatic dependent
 // launch, waits before reading T32).  Chained launches (2) are not supported
-// by this kernel (decode_chain_ok).
+// by this kernel (decode_chain_ok).  ep: as launch_tc_forward.
 // Whether the streaming forward supports chained launches for this M and d_in.
 bool decode_chain_ok(int64_t M, int64_t d_in);
 
 cudaError_t launch_decode_forward(const uint16_t *X, int64_t M, const uint16_t *vals,
                                   const uint8_t *meta, int64_t d_out, int64_t d_in,
                                   const uint16_t *U, const float *T32, int64_t r, uint16_t *Y,
-                                  int pdl_mode, cudaStream_t stream);
+                                  int pdl_mode, cudaStream_t stream, const Epilogue *ep = nullptr);
 
 }  // namespace slr

@@ -14,6 +14,7 @@
 // products U[i, k] T[m, k]) before one warp-shuffle reduction per token, so Y
 // is written exactly once.  Token blocks of MT tokens go to blockIdx.y.
 #include "common.cuh"
+#include "epilogue.cuh"
 
 namespace slr {
 namespace {
@@ -51,11 +52,13 @@ __device__ __forceinline__ float chunk_fma(uint4 v, uint32_t m16, uint4 xa, uint
 
 // 7 resident CTAs of 4 warps per SM (<= 73 registers): 148 x 7 x 4 warps cover
 // the 4096 rows of a Llama-3-8B projection, one row per warp, in one wave.
-template <int MT>
+// kEpi: bias, activation and residual (epilogue.cuh) on the lane that stores a
+// token; their operands are requested before the row's weights.
+template <int MT, bool kEpi>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) decode_forward_kernel(
     const uint16_t *__restrict__ X, int64_t M, const uint16_t *__restrict__ vals,
     const uint8_t *__restrict__ meta, int64_t d_out, int64_t d_in, const uint16_t *__restrict__ U,
-    const float *__restrict__ T32, int64_t r, uint16_t *__restrict__ Y) {
+    const float *__restrict__ T32, int64_t r, uint16_t *Y, const __grid_constant__ Epilogue ep) {
     const int lane = threadIdx.x & 31;
     const int64_t m0 = (int64_t)blockIdx.y * MT;
     const int nt = (int)((M - m0) < MT ? (M - m0) : MT);
@@ -68,6 +71,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) decode_forward_kern
         float acc[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[t] = 0.f;
+        uint32_t bres = 0, bbias = 0;
+        if constexpr (kEpi) {
+            if (ep.res != nullptr && lane < nt) bres = ld_res(ep.res + (m0 + lane) * ep.ldr + row);
+            if (ep.bias != nullptr) bbias = __ldg(ep.bias + row);
+        }
         const uint16_t *vrow = vals + row * (d_in / 2);
         const uint8_t *mrow = meta + row * (d_in / 8);
         // The rank-r operands of this row: U now (it does not depend on the
@@ -150,6 +158,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) decode_forward_kern
 #pragma unroll
             for (int t = 1; t < MT; ++t)
                 if (lane == t) s = acc[t];
+            if constexpr (kEpi) {
+                s += bf16lo_to_f32(bbias);
+                if (ep.pre != nullptr) ep.pre[(m0 + lane) * d_out + row] = f32_to_bf16_bits(s);
+                float z[1] = {s};
+                act_values<1>(z, ep.act);
+                s = z[0] + bf16lo_to_f32(bres);
+            }
             Y[(m0 + lane) * d_out + row] = f32_to_bf16_bits(s);
         }
     }
@@ -158,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) decode_forward_kern
 template <int MT>
 cudaError_t launch_mt(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta, int64_t d_out,
                       int64_t d_in, const uint16_t *U, const float *T32, int64_t r, uint16_t *Y,
-                      bool after_projection, cudaStream_t stream) {
+                      bool after_projection, const Epilogue *ep, cudaStream_t stream) {
     const int64_t tblocks = (M + MT - 1) / MT;
     if (tblocks > 65535) return cudaErrorInvalidConfiguration;
     int dev = 0, sms = 148;
@@ -181,7 +196,9 @@ cudaError_t launch_mt(const uint16_t *X, int64_t M, const uint16_t *vals, const 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after_projection ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_forward_kernel<MT>, X, M, vals, meta, d_out, d_in, U, T32, r, Y);
+    const auto kernel = ep != nullptr ? decode_forward_kernel<MT, true> : decode_forward_kernel<MT, false>;
+    return cudaLaunchKernelEx(&cfg, kernel, X, M, vals, meta, d_out, d_in, U, T32, r, Y,
+                              ep != nullptr ? *ep : Epilogue{});
 }
 
 }  // namespace
@@ -194,12 +211,12 @@ bool decode_chain_ok(int64_t, int64_t) {
 
 cudaError_t launch_decode_forward(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                   int64_t d_out, int64_t d_in, const uint16_t *U, const float *T32, int64_t r,
-                                  uint16_t *Y, int pdl_mode, cudaStream_t stream) {
+                                  uint16_t *Y, int pdl_mode, cudaStream_t stream, const Epilogue *ep) {
     const bool pdl = pdl_mode != 0 && r > 0;
-    if (M <= 1) return launch_mt<1>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, stream);
-    if (M <= 2) return launch_mt<2>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, stream);
-    if (M <= 4) return launch_mt<4>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, stream);
-    return launch_mt<8>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, stream);
+    if (M <= 1) return launch_mt<1>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, ep, stream);
+    if (M <= 2) return launch_mt<2>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, ep, stream);
+    if (M <= 4) return launch_mt<4>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, ep, stream);
+    return launch_mt<8>(X, M, vals, meta, d_out, d_in, U, T32, r, Y, pdl, ep, stream);
 }
 
 }  // namespace slr

@@ -1,0 +1,106 @@
+// epilogue.cuh -- bias, activation and residual of the layer's epilogue, and
+// the activation's slope for its backward pass (internal).
+//
+//   Z = X S^T + T U^T + b          (fp32)
+//   Y = act(Z) + R                 (fp32, rounded to bf16 once)
+//
+// The activations, with u = sqrt(2/pi) (z + 0.044715 z^3):
+//   relu       max(z, 0)                        slope [z > 0]
+//   gelu       z Phi(z) = z erfc(-z/sqrt 2)/2   slope Phi(z) + z phi(z)
+//   gelu_tanh  z (1 + tanh u)/2 = z / (1 + e^-2u)
+//   silu       z / (1 + e^-z)
+// The quotient forms have no cancellation for negative z, where 1 + tanh u
+// would lose every digit; erfc serves the Gaussian distribution function for
+// the same reason.  NaN stays NaN in every one of them.
+#pragma once
+
+#include "common.cuh"
+
+namespace slr {
+
+// Operands of the epilogue (device pointers; bias, res and pre may be null).
+struct Epilogue {
+    const uint16_t *bias;   // bf16 [d_out]
+    const uint16_t *res;    // bf16 [M, ldr]: R, which may be Y itself
+    int64_t ldr;
+    uint16_t *pre;          // bf16 [M, d_out]: Z, out
+    int32_t act;            // slr_act
+};
+
+constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
+constexpr float kInvSqrt2 = 0.7071067811865476f;
+constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+__device__ __forceinline__ float act_gelu(float z) { return 0.5f * z * erfcf(-z * kInvSqrt2); }
+__device__ __forceinline__ float act_gelu_tanh(float z) {
+    const float u = kGeluC * fmaf(0.044715f * z, z * z, z);
+    return __fdividef(z, 1.0f + __expf(-2.0f * u));
+}
+__device__ __forceinline__ float act_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// act over N values; the switch is uniform and outside the loops.
+template <int N>
+__device__ __forceinline__ void act_values(float (&z)[N], int act) {
+    switch (act) {
+        case SLR_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = z[i] <= 0.f ? 0.f : z[i];
+            break;
+        case SLR_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = act_gelu(z[i]);
+            break;
+        case SLR_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = act_gelu_tanh(z[i]);
+            break;
+        case SLR_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = act_silu(z[i]);
+            break;
+        default: break;
+    }
+}
+
+// One bf16 of R: an ordinary coherent load (R may be written by the grid
+// before a chained call, or be the Y that this grid writes).
+__device__ __forceinline__ uint32_t ld_res(const uint16_t *p) {
+    uint16_t v;
+    asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// N tokens of R for one output row, two packed per word (0 past the problem).
+template <int N>
+__device__ __forceinline__ void load_res_row(const Epilogue &ep, int64_t tok0, int64_t M, int64_t row, int64_t d_out,
+                                             uint32_t (&r)[N / 2]) {
+    const bool in = ep.res != nullptr && row < d_out;
+    const uint16_t *p = ep.res + tok0 * ep.ldr + row;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        uint32_t lo = 0, hi = 0;
+        if (in && tok0 + 2 * j < M) lo = ld_res(p + (int64_t)(2 * j) * ep.ldr);
+        if (in && tok0 + 2 * j + 1 < M) hi = ld_res(p + (int64_t)(2 * j + 1) * ep.ldr);
+        r[j] = lo | (hi << 16);
+    }
+}
+
+// N tokens of one output row: z += bias, Z stored (where wanted), act, + R
+// (packed as load_res_row gives it).
+template <int N>
+__device__ __forceinline__ void epilogue_row(const Epilogue &ep, float (&z)[N], float bias, const uint32_t *r,
+                                             int64_t tok0, int64_t M, int64_t row, int64_t d_out) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] += bias;
+    if (ep.pre != nullptr && row < d_out) {
+        uint16_t *p = ep.pre + tok0 * d_out + row;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (tok0 + j < M) p[(int64_t)j * d_out] = f32_to_bf16_bits(z[j]);
+    }
+    act_values<N>(z, ep.act);
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] += (j & 1) ? bf16hi_to_f32(r[j / 2]) : bf16lo_to_f32(r[j / 2]);
+}
+
+}  // namespace slr

@@ -41,6 +41,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "tc_forward.cuh"
 #include "tc_ptx.cuh"
 
@@ -575,9 +576,13 @@ struct SparseCursor {
 
 constexpr int kThreads2 = 256;  // 8 warps
 
-template <int BN>
+// kEpi: the epilogue adds bias, activation and residual (epilogue.cuh); the
+// residual of a 32-token piece is loaded one piece ahead, so that its latency
+// overlaps the arithmetic and the store of the piece before.
+template <int BN, bool kEpi = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
-    tc2_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm) {
+    tc2_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm,
+                       const __grid_constant__ Epilogue ep) {
     using C = Cfg2<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -856,6 +861,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             const int d0 = ch.d0 + (int)rank * BM;
             const int buf = C::NACC == 2 ? (it & 1) : 0;
             const uint32_t use = (uint32_t)(C::NACC == 2 ? (it >> 1) : it);
+            uint32_t rnext[16];
+            float bias = 0.f;
+            if constexpr (kEpi) {
+                if (ep.bias != nullptr && d0 + row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + d0 + row));
+                load_res_row<32>(ep, ch.tok0, min(M, ch.tok0 + ch.n), d0 + row, d_out, rnext);
+            }
             if (!mbar_wait_cluster(&acc_full[buf], use & 1)) {
                 *fail = 1;
                 atomicOr(&g_tc_error, 128u);
@@ -875,6 +886,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                     tmem_ld_32x32b_x16(acc + (uint32_t)(q * 32), h);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = h[j];
+                    if constexpr (kEpi) {
+#pragma unroll
+                        for (int j = 16; j < 32; ++j) v[j] = 0;
+                    }
                 }
                 if (q == nq - 1) {
                     tc_fence_before();
@@ -883,6 +898,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 }
                 const int tq = ch.tok0 + q * C::OUT_COLS;
                 if (tq >= M) continue;  // uniform across the epilogue warps
+                if constexpr (kEpi) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = rnext[j];
+                    if (q + 1 < nq) load_res_row<32>(ep, tq + 32, min(M, ch.tok0 + ch.n), d0 + row, d_out, rnext);
+                    float z[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
+                    // A 16-token piece's other columns belong to the next chunk.
+                    epilogue_row<32>(ep, z, bias, r, tq, min(M, ch.tok0 + ch.n), d0 + row, d_out);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(z[j]);
+                }
                 const uint32_t sb = C::NOUT == 2 ? (piece & 1) : 0u;
                 if (store_thread) {
                     if (C::NOUT == 2)
@@ -986,9 +1014,13 @@ __device__ __forceinline__ bool spin_count_ge(const unsigned int *p, unsigned in
     }
 }
 
-template <int BN>
+// kEpi: bias, activation and residual (epilogue.cuh).  The registers that take
+// the packed outputs hold the residual first, loaded while the chunk's MMAs
+// run.
+template <int BN, bool kEpi = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
-    tc2t_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm) {
+    tc2t_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm,
+                        const __grid_constant__ Epilogue ep) {
     using C = CfgT<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1464,6 +1496,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
                 break;
             }
             const int d0 = ch.d0 + grp * 2 * BM + (int)rank * BM;
+            uint32_t packed[kPieces * 8];
+            float bias = 0.f;
+            if constexpr (kEpi) {
+                if (ep.bias != nullptr && d0 + row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + d0 + row));
+                load_res_row<kPieces * 16>(ep, ch.tok0, min(M, ch.tok0 + ch.n), d0 + row, d_out, packed);
+            }
             if (!mbar_wait_cluster(acc_full, (uint32_t)(it & 1))) {
                 *fail = 1;
                 atomicOr(&g_tc_error, 128u);
@@ -1471,7 +1509,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
             }
             tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(grp * BN);
-            uint32_t packed[kPieces * 8];
             // Two 16-column pieces per TMEM round trip (a piece past the
             // chunk re-reads the last valid one; its values are not used).
 #pragma unroll
@@ -1480,6 +1517,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
                     const int q2 = (q + 1 < kPieces && (q + 1) * 16 < ch.n) ? q + 1 : q;
                     uint32_t h[32];
                     tmem_ld_32x32b_2x16(acc + (uint32_t)(q * 16), acc + (uint32_t)(q2 * 16), h);
+                    if constexpr (kEpi) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            if (q + b < kPieces) {
+                                float z[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(h[16 * b + j]);
+                                const int tq = ch.tok0 + (q + b) * 16;
+                                epilogue_row<16>(ep, z, bias, packed + (q + b) * 8, tq, min(M, ch.tok0 + ch.n),
+                                                 d0 + row, d_out);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) h[16 * b + j] = __float_as_uint(z[j]);
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         packed[q * 8 + j] = (uint32_t)f32_to_bf16_bits(__uint_as_float(h[2 * j])) |
@@ -1569,6 +1621,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
             } else {
                 const float *first = prm.ks_part + (int64_t)(pair - cq) * kKsSlotFloats + sub + 4 * row;
                 const int yrow = d0 + row;
+                float bias = 0.f;
+                if constexpr (kEpi)
+                    if (ep.bias != nullptr && yrow < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + yrow));
                 const int nb = ch.n / 4;
                 const int b0 = (nb * cq) / cg, b1 = (nb * (cq + 1)) / cg;
 #pragma unroll 1
@@ -1602,7 +1657,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
                         for (int u = 0; u < 8; ++u) {
                             const int tok = ch.tok0 + 4 * (b + u);
                             if (b + u < b1) {
-                                const float e4[4] = {sum[u].x, sum[u].y, sum[u].z, sum[u].w};
+                                float e4[4] = {sum[u].x, sum[u].y, sum[u].z, sum[u].w};
+                                if constexpr (kEpi) {
+                                    uint32_t r2[2];
+                                    load_res_row<4>(ep, tok, M, yrow, d_out, r2);
+                                    epilogue_row<4>(ep, e4, bias, r2, tok, M, yrow, d_out);
+                                }
 #pragma unroll
                                 for (int w = 0; w < 4; ++w)
                                     if (tok + w < M) prm.y[(int64_t)(tok + w) * d_out + yrow] = f32_to_bf16_bits(e4[w]);
@@ -1969,8 +2029,10 @@ int64_t plan_check(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int kernel
 template <int BN>
 cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
-                               uint16_t *Y, bool after_projection, int tail_mode, cudaStream_t stream, int chu = 0) {
+                               uint16_t *Y, bool after_projection, int tail_mode, cudaStream_t stream, int chu = 0,
+                               const Epilogue *ep = nullptr) {
     using C = Cfg2<BN>;
+    const auto kernel = ep != nullptr ? tc2_forward_kernel<BN, true> : tc2_forward_kernel<BN, false>;
     if (tail_mode == 2) tail_mode = 1;   // the K split is the 512-row kernel's
     Maps2 maps;
     memset(&maps, 0, sizeof maps);
@@ -1984,7 +2046,7 @@ cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *val
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t err = cudaFuncSetAttribute(tc2_forward_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     Params2 prm;
     int pairs = 0;
@@ -2010,15 +2072,17 @@ cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *val
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (after_projection && r > 0) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tc2_forward_kernel<BN>, maps, prm);
+    return cudaLaunchKernelEx(&cfg, kernel, maps, prm, ep != nullptr ? *ep : Epilogue{});
 }
 
 template <int BN>
 cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
                                uint16_t *Y, bool after_projection, int tail_mode, cudaStream_t stream, int chu = 0,
-                               const uint16_t *V = nullptr, uint8_t *fused_ws = nullptr, size_t ws_bytes = 0) {
+                               const uint16_t *V = nullptr, uint8_t *fused_ws = nullptr, size_t ws_bytes = 0,
+                               const Epilogue *ep = nullptr) {
     using C = CfgT<BN>;
+    const auto kernel = ep != nullptr ? tc2t_forward_kernel<BN, true> : tc2t_forward_kernel<BN, false>;
     // With a fused workspace (single-call forward, r > 0) T lives in its
     // first region; the kernel forms T itself (projection phase) when r <=
     // 128, and the last round may be split along K (partials and counters in
@@ -2042,7 +2106,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t err = cudaFuncSetAttribute(tc2t_forward_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     Params2 prm;
     int pairs = 0;
@@ -2058,7 +2122,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
         occ.gridDim = dim3((unsigned)(2 * max_pairs));
         occ.blockDim = dim3(kThreadsT);
         occ.dynamicSmemBytes = C::SMEM;
-        err = cudaOccupancyMaxActiveClusters(&ncl, tc2t_forward_kernel<BN>, &occ);
+        err = cudaOccupancyMaxActiveClusters(&ncl, kernel, &occ);
         if (err != cudaSuccess) return err;
         if (ncl < max_pairs) max_pairs = ncl;
         if (max_pairs < 1) return cudaErrorInvalidConfiguration;
@@ -2128,7 +2192,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (after_projection && r > 0 && !tp) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tc2t_forward_kernel<BN>, maps, prm);
+    return cudaLaunchKernelEx(&cfg, kernel, maps, prm, ep != nullptr ? *ep : Epilogue{});
 }
 
 
@@ -2434,12 +2498,15 @@ struct CfgS {
     static_assert(BN % 16 == 0 && BN <= 128, "MMA N");
 };
 
-template <int BN>
+// kEpi: bias, activation and residual (epilogue.cuh) in the reduction over the
+// cluster.  A thread's first four residual values are loaded before it waits
+// for the MMAs, after the wait for the preceding grid in a chained launch.
+template <int BN, bool kEpi = false>
 __global__ void __launch_bounds__(kThreads, 2)
     tc_small_kernel(const __grid_constant__ CUtensorMap tm_vals, const __grid_constant__ CUtensorMap tm_meta,
                     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_u,
                     const __grid_constant__ CUtensorMap tm_t, uint16_t *__restrict__ Y, int32_t M, int32_t d_out,
-                    int32_t n_ttiles, int32_t nk, int32_t nlr, int32_t pdl) {
+                    int32_t n_ttiles, int32_t nk, int32_t nlr, int32_t pdl, const __grid_constant__ Epilogue ep) {
     using C = CfgS<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -2488,6 +2555,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         asm volatile("bar.sync 1, %0;" ::"r"(kThreads) : "memory");
         tc_fence_after();
         tmem_base = *tmem_slot;
+    }
+
+    uint32_t r2[2] = {0, 0};
+    if constexpr (kEpi) {
+        if (warp >= 2 && ep.res != nullptr) {
+            if (pdl == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+            const int it = threadIdx.x - 64, rpc = BM / (int)ks_n;
+            if (it < rpc * (BN / 4))
+                load_res_row<4>(ep, tok0 + 4 * (it / rpc), M, d0 + (int)ks_q * rpc + it % rpc, d_out, r2);
+        }
     }
 
     if (warp == 0) {
@@ -2639,9 +2716,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (uint32_t q = 0; q < 4; ++q)
                 p[q] = q < ks_n ? ld_shared_cluster_v4(mapa_shared(part_addr + off, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float sum[4] = {p[0].x + p[1].x + p[2].x + p[3].x, p[0].y + p[1].y + p[2].y + p[3].y,
-                                  p[0].z + p[1].z + p[2].z + p[3].z, p[0].w + p[1].w + p[2].w + p[3].w};
+            float sum[4] = {p[0].x + p[1].x + p[2].x + p[3].x, p[0].y + p[1].y + p[2].y + p[3].y,
+                            p[0].z + p[1].z + p[2].z + p[3].z, p[0].w + p[1].w + p[2].w + p[3].w};
             const int out_row = d0 + row;
+            if constexpr (kEpi) {
+                const int tq = tok0 + 4 * tg;
+                float bias = 0.f;
+                if (ep.bias != nullptr && out_row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + out_row));
+                if (it >= 128) load_res_row<4>(ep, tq, M, out_row, d_out, r2);
+                epilogue_row<4>(ep, sum, bias, r2, tq, M, out_row, d_out);
+            }
             if (out_row < d_out) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -2663,8 +2747,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <int BN>
 cudaError_t launch_sparse_small(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                 int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
-                                uint16_t *Y, int pdl, cudaStream_t stream) {
+                                uint16_t *Y, int pdl, cudaStream_t stream, const Epilogue *ep = nullptr) {
     using C = CfgS<BN>;
+    const auto kernel = ep != nullptr ? tc_small_kernel<BN, true> : tc_small_kernel<BN, false>;
     CUtensorMap m_vals, m_meta, m_x, m_u, m_t;
     memset(&m_u, 0, sizeof m_u);
     memset(&m_t, 0, sizeof m_t);
@@ -2683,7 +2768,7 @@ cudaError_t launch_sparse_small(const uint16_t *X, int64_t M, const uint16_t *va
     const int work = (int)((d_out + BM - 1) / BM) * n_ttiles;
     const int nk = (int)(d_in / BK), nlr = (int)((r + 63) / 64);
     const int ks = small_cluster(work, nk + nlr, sms);
-    cudaError_t err = cudaFuncSetAttribute(tc_small_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(work * ks));
@@ -2700,15 +2785,16 @@ cudaError_t launch_sparse_small(const uint16_t *X, int64_t M, const uint16_t *va
     cfg.attrs = attr;
     const int mode = (pdl == 1 && r == 0) ? 0 : pdl;
     cfg.numAttrs = mode != 0 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, tc_small_kernel<BN>, m_vals, m_meta, m_x, m_u, m_t, Y, (int32_t)M,
-                              (int32_t)d_out, (int32_t)n_ttiles, (int32_t)nk, (int32_t)nlr, (int32_t)mode);
+    return cudaLaunchKernelEx(&cfg, kernel, m_vals, m_meta, m_x, m_u, m_t, Y, (int32_t)M, (int32_t)d_out,
+                              (int32_t)n_ttiles, (int32_t)nk, (int32_t)nlr, (int32_t)mode,
+                              ep != nullptr ? *ep : Epilogue{});
 }
 
 }  // namespace tc
 
 cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                               int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
-                              uint16_t *Y, int pdl, cudaStream_t stream) {
+                              uint16_t *Y, int pdl, cudaStream_t stream, const Epilogue *ep) {
     if (M <= 0) return cudaSuccess;
     if (M > INT32_MAX || d_out > INT32_MAX || d_in > INT32_MAX) return cudaErrorInvalidValue;
     // Chained launches (pdl == 2) exist for the split-K kernel of M <= 64 only.
@@ -2719,22 +2805,22 @@ cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals
     // measurements.
     const char *force = getenv("SLR_TC_KERNEL");
     if (force != nullptr) {
-        if (strcmp(force, "1sm") == 0) return tc::launch_sparse<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, stream);
+        if (strcmp(force, "1sm") == 0 && ep == nullptr) return tc::launch_sparse<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, stream);
         const bool whole = force[0] != 0 && force[strlen(force) - 1] == 'w';
         const int tail = whole ? 0 : 1;
         if (strncmp(force, "2sm128", 6) == 0)
-            return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
+            return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, ep);
         if (strncmp(force, "2sm256", 6) == 0)
-            return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
+            return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, ep);
         if (strncmp(force, "2sm240", 6) == 0)
-            return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
+            return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, ep);
         if (strncmp(force, "2smtall", 7) == 0)
-            return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
+            return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, nullptr, nullptr, 0, ep);
         if (strcmp(force, "small") == 0) {
-            if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
-            if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
-            if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
-            return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+            if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+            if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+            if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+            return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
         }
     }
     // Up to 64 tokens the layer streams S: the split-K kernel.  Above, the
@@ -2745,26 +2831,26 @@ cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals
     // chunks; each with the last round split among all pairs or dealt as whole
     // tiles.  The pair plan with the smallest estimated time of its slowest
     // pair is launched.
-    if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
-    if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
-    if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+    if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+    if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+    if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (tc::small_wins(M, d_out, d_in, sms))
-        return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+        return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
     const tc::PlanChoice c = tc::choose_plan(M, d_out, d_in, r, sms, false);
     if (c.kind == 0)
-        return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
+        return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, ep);
     if (c.kind == 1)
-        return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
+        return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, ep);
     if (c.kind == 3)
-        return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
-    return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
+        return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, ep);
+    return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, nullptr, nullptr, 0, ep);
 }
 
 cudaError_t launch_tc_forward_fused(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                     int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *V, int64_t r,
-                                    uint16_t *Y, uint8_t *ws, size_t ws_bytes, cudaStream_t stream) {
+                                    uint16_t *Y, uint8_t *ws, size_t ws_bytes, cudaStream_t stream, const Epilogue *ep) {
     if (M <= 0) return cudaSuccess;
     if (M > INT32_MAX || d_out > INT32_MAX || d_in > INT32_MAX) return cudaErrorInvalidValue;
     uint16_t *T16 = reinterpret_cast<uint16_t *>(ws);
@@ -2793,10 +2879,10 @@ cudaError_t launch_tc_forward_fused(const uint16_t *X, int64_t M, const uint16_t
     }
     if (tail >= 0)
         return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, false, tail, stream, chu, V,
-                                           ws, ws_bytes);
+                                           ws, ws_bytes, ep);
     cudaError_t err = cudaSuccess;
     if (r > 0) err = launch_tc_project(X, M, V, d_in, r, T16, false, stream);
-    if (err == cudaSuccess) err = launch_tc_forward(X, M, vals, meta, d_out, d_in, U, r > 0 ? T16 : nullptr, r, Y, 1, stream);
+    if (err == cudaSuccess) err = launch_tc_forward(X, M, vals, meta, d_out, d_in, U, r > 0 ? T16 : nullptr, r, Y, 1, stream, ep);
     return err;
 }
 

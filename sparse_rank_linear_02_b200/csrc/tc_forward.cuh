@@ -7,6 +7,8 @@
 
 namespace slr {
 
+struct Epilogue;   // epilogue.cuh
+
 namespace tc {
 // 2-D tiled tensor map of a row-major matrix (inner x outer elements, row
 // pitch row_bytes) with the given box and swizzle; false when the driver's
@@ -55,9 +57,11 @@ inline FusedLayout fused_layout(int64_t M, int64_t r, int64_t pairs) {
 // waits before reading T16); 2 = chained (M <= kChainMaxM): also the work
 // before the projection may still be running, so the kernel requests only
 // the weights (S, U) before it waits, and reads X and T16 after.
+// ep: bias, activation, residual and the pre-activation's copy (null: Y is the
+// product itself; the 1-SM variant has no other form).
 cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                               int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
-                              uint16_t *Y, int pdl, cudaStream_t stream);
+                              uint16_t *Y, int pdl, cudaStream_t stream, const Epilogue *ep = nullptr);
 
 // The single-call forward on the tensor cores (M > kChainMaxM): where the
 // dispatch picks the 512-row pair kernel, that kernel with its projection phase
@@ -69,7 +73,8 @@ cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals
 // a K-split plan needs, the last round is split by tokens instead.
 cudaError_t launch_tc_forward_fused(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                     int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *V, int64_t r,
-                                    uint16_t *Y, uint8_t *ws, size_t ws_bytes, cudaStream_t stream);
+                                    uint16_t *Y, uint8_t *ws, size_t ws_bytes, cudaStream_t stream,
+                                    const Epilogue *ep = nullptr);
 
 // T = X V^T on the tensor cores, written as bf16 [M, r] (dense tcgen05 mode of
 // the same kernel).  Requires d_in % 64 == 0, r % 8 == 0.  chained: launched
