@@ -417,8 +417,9 @@ SLR_API slr_status slr_forward_ex(const void *X, int64_t M, const void *vals, co
  * for bit.
  *
  * Accuracy: Z as slr_forward's product; the activation is evaluated in fp32.
- * Requirements: those of slr_forward_ex; bias and R may have any alignment
- * that their type has (2 bytes), Z the same.
+ * Requirements: those of slr_forward_ex; bias may have any alignment that its
+ * type has (2 bytes), R and Z are 16-byte aligned; on the tensor-core path ldr
+ * is a multiple of 8 (M > 1).
  * ------------------------------------------------------------------------ */
 typedef enum slr_act {
     SLR_ACT_NONE = 0,

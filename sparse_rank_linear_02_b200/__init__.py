@@ -146,44 +146,48 @@ def _check(status: int, what: str):
         raise SlrError(status, what)
 
 
-def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, like: torch.Tensor):
+def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device: torch.device):
     """Refuse an operand whose type, shape, layout or device is not what the call reads."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}, not "
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, not "
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _expect_current(t: torch.Tensor):
-    """The kernels run on the current device's current stream, where the operands have to be."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"the operands are on {t.device}, not on the current CUDA device")
+def _current(t: torch.Tensor) -> tuple[torch.device, int]:
+    """The operand's device, which has to be the current one, and its current stream."""
+    device = t.device
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the operands are on {device}, not on the current CUDA device")
+    return device, torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _addr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _expect_layer(vals: torch.Tensor, meta: torch.Tensor, U: torch.Tensor | None, V: torch.Tensor | None,
-                  like: torch.Tensor) -> tuple[int, int, int]:
+                  device: torch.device) -> tuple[int, int, int]:
     """(d_out, d_in, r) of a packed layer, its operands checked."""
     if vals.dim() != 2 or (U is None) != (V is None):
         raise ValueError("vals must be 2-D, and U and V come together")
-    d_out, d_in = vals.shape[0], 2 * vals.shape[1]
-    _expect("vals", vals, torch.bfloat16, (d_out, d_in // 2), like)
-    _expect("meta", meta, torch.uint8, (d_out, meta_row_bytes(d_in)), like)
+    d_out, half = vals.shape
+    _expect("vals", vals, torch.bfloat16, (d_out, half), device)
+    _expect("meta", meta, torch.uint8, (d_out, (half + 3) // 4), device)
     if U is None:
-        return d_out, d_in, 0
+        return d_out, 2 * half, 0
     r = V.shape[0]
-    _expect("U", U, torch.bfloat16, (d_out, r), like)
-    _expect("V", V, torch.bfloat16, (r, d_in), like)
-    return d_out, d_in, r
+    _expect("U", U, torch.bfloat16, (d_out, r), device)
+    _expect("V", V, torch.bfloat16, (r, 2 * half), device)
+    return d_out, 2 * half, r
 
 
-def _scratch(workspace: torch.Tensor | None, need: int, like: torch.Tensor) -> tuple[torch.Tensor | None, int]:
-    """The caller's workspace, or a new one where the call needs it, and its bytes."""
+def _scratch(workspace: torch.Tensor | None, need: int, device: torch.device) -> tuple[torch.Tensor | None, int]:
+    """The caller's workspace, or a new one of `need` bytes, and its bytes."""
     if workspace is None:
-        if need == 0:
-            return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif not workspace.is_contiguous() or workspace.device != like.device:
-        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.nbytes
 
 
 def meta_row_bytes(d_in: int) -> int:
@@ -389,31 +393,32 @@ def forward_epilogue(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, U:
     :func:`forward`'s (:func:`workspace_size`)."""
     if X.dim() != 2 or act not in ACTS:
         raise ValueError(f"X must be 2-D and act one of {', '.join(ACTS)}")
-    _expect_current(X)
+    device, stream = _current(X)
     M = X.shape[0]
-    d_out, d_in, r = _expect_layer(vals, meta, U, V, X)
-    _expect("X", X, torch.bfloat16, (M, d_in), X)
+    d_out, d_in, r = _expect_layer(vals, meta, U, V, device)
+    _expect("X", X, torch.bfloat16, (M, d_in), device)
     if out is None:
-        out = torch.empty((M, d_out), dtype=torch.bfloat16, device=X.device)
+        out = torch.empty((M, d_out), dtype=torch.bfloat16, device=device)
     else:
-        _expect("out", out, torch.bfloat16, (M, d_out), X)
+        _expect("out", out, torch.bfloat16, (M, d_out), device)
     if bias is not None:
-        _expect("bias", bias, torch.bfloat16, (d_out,), X)
+        _expect("bias", bias, torch.bfloat16, (d_out,), device)
     if preact is not None:
-        _expect("preact", preact, torch.bfloat16, (M, d_out), X)
+        _expect("preact", preact, torch.bfloat16, (M, d_out), device)
     ldr = d_out
     if residual is not None:
-        if residual.dtype != torch.bfloat16 or residual.shape != (M, d_out) or residual.device != X.device or \
+        if residual.dtype is not torch.bfloat16 or residual.shape != (M, d_out) or residual.device != device or \
                 (d_out > 1 and residual.stride(1) != 1):
-            raise ValueError(f"residual must be a bf16 tensor of shape {(M, d_out)} on {X.device} with unit column "
-                             f"stride")
+            raise ValueError(f"residual must be a bf16 tensor of shape {(M, d_out)} on {device} with unit column stride")
         if M > 1:
             ldr = residual.stride(0)
-    ws, ws_bytes = _scratch(workspace, workspace_size(M, d_out, d_in, r), X)
-    flags = FWD_OVERLAP_PRECEDING if overlap_preceding else 0
-    _check(_lib.slr_forward_epilogue(_ptr(X), M, _ptr(vals), _ptr(meta), d_out, d_in, _ptr(U), _ptr(V), r, _ptr(bias),
-                                     ACTS[act], _ptr(residual), ldr, _ptr(preact), _ptr(out), _ptr(ws), ws_bytes,
-                                     PATHS[path], flags, _stream()), "slr_forward_epilogue")
+    # The library checks a given workspace's size; only a new one needs to know it here.
+    workspace, ws_bytes = _scratch(workspace, 0 if workspace is not None else workspace_size(M, d_out, d_in, r), device)
+    _check(_lib.slr_forward_epilogue(X.data_ptr(), M, vals.data_ptr(), meta.data_ptr(), d_out, d_in, _addr(U), _addr(V),
+                                     r, _addr(bias), ACTS[act], _addr(residual), ldr, _addr(preact), out.data_ptr(),
+                                     _addr(workspace), ws_bytes, PATHS[path],
+                                     FWD_OVERLAP_PRECEDING if overlap_preceding else 0, stream),
+           "slr_forward_epilogue")
     return out
 
 

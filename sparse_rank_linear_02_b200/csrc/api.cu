@@ -487,7 +487,10 @@ slr_status slr_forward_epilogue(const void *X, int64_t M, const void *vals, cons
                                 slr_path path, uint32_t flags, slr_stream_t stream) {
     if (!slr::act_ok(act)) return SLR_ERR_ARG;
     if (R != nullptr && (ldr < d_out || (R == Y && ldr != d_out))) return SLR_ERR_SHAPE;
-    if (!slr::aligned2(bias) || !slr::aligned2(R) || !slr::aligned2(Z)) return SLR_ERR_ALIGN;
+    // The tensor-core path loads R by TMA, whose row pitch is a multiple of 16 bytes.
+    if (R != nullptr && M > 1 && ldr % 8 != 0 && slr::resolve(path, M, d_out, d_in) == SLR_PATH_TENSOR)
+        return SLR_ERR_SHAPE;
+    if (!slr::aligned2(bias) || !slr::aligned16(R) || !slr::aligned16(Z)) return SLR_ERR_ALIGN;
     slr::Epilogue ep;
     ep.bias = static_cast<const uint16_t *>(bias);
     ep.res = static_cast<const uint16_t *>(R);

@@ -63,44 +63,46 @@ __device__ __forceinline__ void act_values(float (&z)[N], int act) {
 }
 
 // One bf16 of R: an ordinary coherent load (R may be written by the grid
-// before a chained call, or be the Y that this grid writes).
+// before a chained call, or be the Y that this grid writes), kept in order with
+// griddepcontrol.wait by being volatile.
 __device__ __forceinline__ uint32_t ld_res(const uint16_t *p) {
     uint16_t v;
-    asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 
-// N tokens of R for one output row, two packed per word (0 past the problem).
+// N tokens of R for one output row, two packed per word.  Tokens and rows past
+// the problem read its last ones (their outputs are not stored): without
+// branches the loads go out together.
 template <int N>
-__device__ __forceinline__ void load_res_row(const Epilogue &ep, int64_t tok0, int64_t M, int64_t row, int64_t d_out,
+__device__ __forceinline__ void load_res_row(const Epilogue &ep, int tok0, int M, int row, int d_out,
                                              uint32_t (&r)[N / 2]) {
-    const bool in = ep.res != nullptr && row < d_out;
-    const uint16_t *p = ep.res + tok0 * ep.ldr + row;
+    const uint16_t *p = ep.res + min(row, d_out - 1);
+    uint32_t v[N];
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-        uint32_t lo = 0, hi = 0;
-        if (in && tok0 + 2 * j < M) lo = ld_res(p + (int64_t)(2 * j) * ep.ldr);
-        if (in && tok0 + 2 * j + 1 < M) hi = ld_res(p + (int64_t)(2 * j + 1) * ep.ldr);
-        r[j] = lo | (hi << 16);
-    }
+    for (int j = 0; j < N; ++j) v[j] = ld_res(p + (int64_t)min(tok0 + j, M - 1) * ep.ldr);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) r[j] = v[2 * j] | (v[2 * j + 1] << 16);
 }
 
 // N tokens of one output row: z += bias, Z stored (where wanted), act, + R
-// (packed as load_res_row gives it).
+// (packed as load_res_row gives it; null: none).
 template <int N>
 __device__ __forceinline__ void epilogue_row(const Epilogue &ep, float (&z)[N], float bias, const uint32_t *r,
-                                             int64_t tok0, int64_t M, int64_t row, int64_t d_out) {
+                                             int tok0, int M, int row, int d_out) {
 #pragma unroll
     for (int j = 0; j < N; ++j) z[j] += bias;
     if (ep.pre != nullptr && row < d_out) {
-        uint16_t *p = ep.pre + tok0 * d_out + row;
+        uint16_t *p = ep.pre + (int64_t)tok0 * d_out + row;
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (tok0 + j < M) p[(int64_t)j * d_out] = f32_to_bf16_bits(z[j]);
     }
     act_values<N>(z, ep.act);
+    if (r != nullptr) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) z[j] += (j & 1) ? bf16hi_to_f32(r[j / 2]) : bf16lo_to_f32(r[j / 2]);
+        for (int j = 0; j < N; ++j) z[j] += (j & 1) ? bf16hi_to_f32(r[j / 2]) : bf16lo_to_f32(r[j / 2]);
+    }
 }
 
 }  // namespace slr

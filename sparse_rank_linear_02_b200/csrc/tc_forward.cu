@@ -363,7 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   mempty[m]    leader's commit after the MMAs that read slot m, multicast
 //   acc_full[b]  leader's commit, multicast
 //   acc_empty[b] 8 epilogue warps (both CTAs) -> leader: buffer drained
-template <int BN>
+// kEpi: the output staging is six 16-token pieces (three for each of the two
+// epilogue groups) instead of up to two of 32 tokens.
+template <int BN, bool kEpi = false>
 struct Cfg2 {
     static constexpr int HALF_N = BN / 2;               // most tokens staged per CTA
     static constexpr int CHU = BN / 16;                 // most 16-token units per chunk
@@ -386,7 +388,7 @@ struct Cfg2 {
     static constexpr int FIXED1 = MS * E_BYTES + 1024 + 16 * MS + 16;
     static constexpr int AVAIL = 232448 - 1024 - FIXED1;
     // Two output staging buffers unless dropping one buys another stage.
-    static constexpr int NOUT = ((AVAIL - 2 * OUT_BYTES) / STAGE < (AVAIL - OUT_BYTES) / STAGE) ? 1 : 2;
+    static constexpr int NOUT = kEpi ? 3 : ((AVAIL - 2 * OUT_BYTES) / STAGE < (AVAIL - OUT_BYTES) / STAGE) ? 1 : 2;
     static constexpr int NS_FIT = (AVAIL - NOUT * OUT_BYTES) / STAGE;
     static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;
     static constexpr int RING = NS * STAGE;
@@ -401,7 +403,7 @@ struct Cfg2 {
     static_assert(MLEAD < MS && MLEAD % 2 == 0 && MS % 2 == 0, "metadata lead");
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(ECOL + 4 <= TMEM_COLS, "TMEM budget");
-    static_assert((2 * NS + 3 * MS + 4) * 8 + 8 <= 1024, "barrier area");
+    static_assert((2 * NS + 3 * MS + 8) * 8 + 8 <= 1024, "barrier area");
 };
 
 // Tensor maps of the 2-SM kernel.  xs[i] loads box_rows(i) rows of X for both
@@ -576,14 +578,44 @@ struct SparseCursor {
 
 constexpr int kThreads2 = 256;  // 8 warps
 
-// kEpi: the epilogue adds bias, activation and residual (epilogue.cuh); the
-// residual of a 32-token piece is loaded one piece ahead, so that its latency
-// overlaps the arithmetic and the store of the piece before.
+// Operands of the epilogue form: residual and pre-activation in boxes of 16
+// tokens x 128 rows.
+struct EpiArgs2 {
+    Epilogue ep;
+    CUtensorMap r16, z16;
+};
+struct NoEpiArgs2 {};
+constexpr int kThreads2E = 384;  // 12 warps
+
+// Bounded-wait verdicts of a group's threads, joined: all of them go on or none
+// does, so that no named barrier is left waiting for a thread that gave up.
+__device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t n, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(n), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+}
+
+// kEpi: bias, activation, residual and the copy of the pre-activation
+// (epilogue.cuh).  Two groups of four warps (2..5 and 8..11) take the chunk's
+// 16-token units in turn, so that the activation's arithmetic stays beside the
+// MMAs of the next chunk: with one group of four the epilogue of a 240-token
+// chunk with GELU took longer than the 32 stages of a 4096-wide layer.  A
+// residual unit comes by TMA into the piece of shared memory that its outputs
+// then overwrite, one unit ahead; outputs leave by TMA (reading and writing
+// them with 2-byte accesses per thread took 473 us against 133 us for the
+// 14336 x 4096 layer at 2048 tokens).
 template <int BN, bool kEpi = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEpi ? kThreads2E : kThreads2, 1)
     tc2_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm,
-                       const __grid_constant__ Epilogue ep) {
-    using C = Cfg2<BN>;
+                       const __grid_constant__ std::conditional_t<kEpi, EpiArgs2, NoEpiArgs2> ea) {
+    using C = Cfg2<BN, kEpi>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
@@ -593,7 +625,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
     uint64_t *mempty = mready + C::MS;
     uint64_t *acc_full = mempty + C::MS;
     uint64_t *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *rfull = acc_empty + 2;   // kEpi: residual piece landed, [group][2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rfull + 4);
     volatile uint32_t *fail = tmem_slot + 1;
     uint8_t *meta_ring = smem + C::META_OFF;
     uint8_t *dummy = smem + C::DUMMY_OFF;   // MS signal slots + 1 source slot
@@ -621,8 +654,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], kEpi ? 16 : 8);
         }
+        if (kEpi)
+            for (int b = 0; b < 4; ++b) mbar_init(&rfull[b], 1);
         *fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -701,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 }
             }
         }
-    } else if (warp >= 6) {
+    } else if (warp == 6 || warp == 7) {
         // ------------------------------------------------------------ metadata warps (each CTA)
         // Warp 6 takes the even sparse stages, warp 7 the odd ones; each loads
         // its tiles MLEAD stages ahead into slots of its own parity.
@@ -846,6 +881,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 ++it;
             }
         }
+    } else if constexpr (kEpi) {
+        // ------------------------------------------------------------ epilogue with bias, activation, residual
+        const Epilogue &ep = ea.ep;
+        const int grp = warp >= 8 ? 1 : 0;
+        const int row = (warp & 3) * 32 + lane;
+        const bool store_thread = (warp & 3) == 2 - 2 * grp && lane == 0;   // warps 2 and 8
+        uint8_t *pieces = smem + C::OUT_OFF + grp * 3 * (C::OUT_BYTES / 2);
+        uint16_t *zbuf = reinterpret_cast<uint16_t *>(pieces + 2 * (C::OUT_BYTES / 2));
+        uint64_t *rbar = rfull + 2 * grp;
+        const uint32_t empty_leader0 = mapa_shared(smem_u32(&acc_empty[0]), 0);
+        const bool res = ep.res != nullptr, pre = ep.pre != nullptr;
+        uint32_t k = 0;    // units of this group so far: piece k & 1, its residual barrier's phase k >> 1
+        int it = 0;
+        bool ok = true;
+        ChunkIter iter(prm, pair, npairs);
+        Chunk ch;
+        // The residual of the unit whose count is kk: into a piece whose last
+        // store has been read (the caller waits for that).
+        auto load_res = [&](uint32_t kk, int d0, int tok) {
+            mbar_expect_tx(&rbar[kk & 1], C::OUT_BYTES / 2);
+            tma_load_2d(&ea.r16, smem_u32(pieces + (kk & 1) * (C::OUT_BYTES / 2)), &rbar[kk & 1], d0, tok);
+        };
+        while (ok && iter.next(prm.chu, ch)) {
+            const int d0 = ch.d0 + (int)rank * BM;
+            const int buf = C::NACC == 2 ? (it & 1) : 0;
+            const uint32_t use = (uint32_t)(C::NACC == 2 ? (it >> 1) : it);
+            const int nu = ch.n / 16;
+            float bias = 0.f;
+            if (ep.bias != nullptr && d0 + row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + d0 + row));
+            if (store_thread && res && grp < nu) {
+                bulk_wait_read0();
+                load_res(k, d0, ch.tok0 + grp * 16);
+            }
+            bool got = *fail == 0 && mbar_wait_cluster(&acc_full[buf], use & 1);
+            tc_fence_after();
+            const uint32_t acc = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (buf ? C::ACC1 : 0u);
+            const uint32_t acc_bar = empty_leader0 + (uint32_t)(buf * sizeof(uint64_t));
+            if (grp >= nu) {   // a 16-token chunk: nothing to read
+                tc_fence_before();
+                if (lane == 0) mbar_arrive_remote_relaxed(acc_bar);
+            }
+#pragma unroll 1
+            for (int u = grp; u < nu; u += 2, ++k) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(acc + (uint32_t)(u * 16), v);
+                if (u + 2 >= nu) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_relaxed(acc_bar);
+                }
+                if (got && res) got = mbar_wait(&rbar[k & 1], (k >> 1) & 1);
+                if (store_thread) {
+                    bulk_wait_read0();   // the unit before is read: its pieces are free
+                    if (got && res && u + 2 < nu) load_res(k + 1, d0, ch.tok0 + (u + 2) * 16);
+                }
+                ok = named_bar_and(1 + grp, 128, got);
+                if (!ok) {
+                    *fail = 1;
+                    if (lane == 0) atomicOr(&g_tc_error, 128u);
+                    break;
+                }
+                uint16_t *out = reinterpret_cast<uint16_t *>(pieces + (k & 1) * (C::OUT_BYTES / 2)) + row;
+                float z[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]) + bias;
+                if (pre) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) zbuf[j * BM + row] = f32_to_bf16_bits(z[j]);
+                }
+                act_values<16>(z, ep.act);
+                if (res) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) z[j] += bf16lo_to_f32(out[j * BM]);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) out[j * BM] = f32_to_bf16_bits(z[j]);
+                fence_proxy_async_smem();
+                named_bar_sync(1 + grp, 128);
+                if (store_thread) {
+                    const int tq = ch.tok0 + u * 16;
+                    if (pre) tma_store_2d(&ea.z16, smem_u32(zbuf), d0, tq);
+                    tma_store_2d(&maps.y16, smem_u32(out - row), d0, tq);
+                    bulk_commit();
+                }
+            }
+            ++it;
+        }
+        if (store_thread) bulk_wait_all();
     } else {
         // ------------------------------------------------------------ epilogue (each CTA, its 128 rows)
         const int quarter = warp & 3;
@@ -861,12 +984,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             const int d0 = ch.d0 + (int)rank * BM;
             const int buf = C::NACC == 2 ? (it & 1) : 0;
             const uint32_t use = (uint32_t)(C::NACC == 2 ? (it >> 1) : it);
-            uint32_t rnext[16];
-            float bias = 0.f;
-            if constexpr (kEpi) {
-                if (ep.bias != nullptr && d0 + row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + d0 + row));
-                load_res_row<32>(ep, ch.tok0, min(M, ch.tok0 + ch.n), d0 + row, d_out, rnext);
-            }
             if (!mbar_wait_cluster(&acc_full[buf], use & 1)) {
                 *fail = 1;
                 atomicOr(&g_tc_error, 128u);
@@ -886,10 +1003,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                     tmem_ld_32x32b_x16(acc + (uint32_t)(q * 32), h);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = h[j];
-                    if constexpr (kEpi) {
-#pragma unroll
-                        for (int j = 16; j < 32; ++j) v[j] = 0;
-                    }
                 }
                 if (q == nq - 1) {
                     tc_fence_before();
@@ -898,19 +1011,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 }
                 const int tq = ch.tok0 + q * C::OUT_COLS;
                 if (tq >= M) continue;  // uniform across the epilogue warps
-                if constexpr (kEpi) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = rnext[j];
-                    if (q + 1 < nq) load_res_row<32>(ep, tq + 32, min(M, ch.tok0 + ch.n), d0 + row, d_out, rnext);
-                    float z[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
-                    // A 16-token piece's other columns belong to the next chunk.
-                    epilogue_row<32>(ep, z, bias, r, tq, min(M, ch.tok0 + ch.n), d0 + row, d_out);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(z[j]);
-                }
                 const uint32_t sb = C::NOUT == 2 ? (piece & 1) : 0u;
                 if (store_thread) {
                     if (C::NOUT == 2)
@@ -1014,13 +1114,9 @@ __device__ __forceinline__ bool spin_count_ge(const unsigned int *p, unsigned in
     }
 }
 
-// kEpi: bias, activation and residual (epilogue.cuh).  The registers that take
-// the packed outputs hold the residual first, loaded while the chunk's MMAs
-// run.
-template <int BN, bool kEpi = false>
+template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
-    tc2t_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm,
-                        const __grid_constant__ Epilogue ep) {
+    tc2t_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm) {
     using C = CfgT<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1496,12 +1592,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
                 break;
             }
             const int d0 = ch.d0 + grp * 2 * BM + (int)rank * BM;
-            uint32_t packed[kPieces * 8];
-            float bias = 0.f;
-            if constexpr (kEpi) {
-                if (ep.bias != nullptr && d0 + row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + d0 + row));
-                load_res_row<kPieces * 16>(ep, ch.tok0, min(M, ch.tok0 + ch.n), d0 + row, d_out, packed);
-            }
             if (!mbar_wait_cluster(acc_full, (uint32_t)(it & 1))) {
                 *fail = 1;
                 atomicOr(&g_tc_error, 128u);
@@ -1509,6 +1599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
             }
             tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(grp * BN);
+            uint32_t packed[kPieces * 8];
             // Two 16-column pieces per TMEM round trip (a piece past the
             // chunk re-reads the last valid one; its values are not used).
 #pragma unroll
@@ -1517,21 +1608,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
                     const int q2 = (q + 1 < kPieces && (q + 1) * 16 < ch.n) ? q + 1 : q;
                     uint32_t h[32];
                     tmem_ld_32x32b_2x16(acc + (uint32_t)(q * 16), acc + (uint32_t)(q2 * 16), h);
-                    if constexpr (kEpi) {
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            if (q + b < kPieces) {
-                                float z[16];
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(h[16 * b + j]);
-                                const int tq = ch.tok0 + (q + b) * 16;
-                                epilogue_row<16>(ep, z, bias, packed + (q + b) * 8, tq, min(M, ch.tok0 + ch.n),
-                                                 d0 + row, d_out);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) h[16 * b + j] = __float_as_uint(z[j]);
-                            }
-                        }
-                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         packed[q * 8 + j] = (uint32_t)f32_to_bf16_bits(__uint_as_float(h[2 * j])) |
@@ -1621,9 +1697,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
             } else {
                 const float *first = prm.ks_part + (int64_t)(pair - cq) * kKsSlotFloats + sub + 4 * row;
                 const int yrow = d0 + row;
-                float bias = 0.f;
-                if constexpr (kEpi)
-                    if (ep.bias != nullptr && yrow < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + yrow));
                 const int nb = ch.n / 4;
                 const int b0 = (nb * cq) / cg, b1 = (nb * (cq + 1)) / cg;
 #pragma unroll 1
@@ -1657,12 +1730,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
                         for (int u = 0; u < 8; ++u) {
                             const int tok = ch.tok0 + 4 * (b + u);
                             if (b + u < b1) {
-                                float e4[4] = {sum[u].x, sum[u].y, sum[u].z, sum[u].w};
-                                if constexpr (kEpi) {
-                                    uint32_t r2[2];
-                                    load_res_row<4>(ep, tok, M, yrow, d_out, r2);
-                                    epilogue_row<4>(ep, e4, bias, r2, tok, M, yrow, d_out);
-                                }
+                                const float e4[4] = {sum[u].x, sum[u].y, sum[u].z, sum[u].w};
 #pragma unroll
                                 for (int w = 0; w < 4; ++w)
                                     if (tok + w < M) prm.y[(int64_t)(tok + w) * d_out + yrow] = f32_to_bf16_bits(e4[w]);
@@ -1909,11 +1977,14 @@ struct PlanChoice {
     int tail;   // plan_pairs' tail_mode
 };
 
-PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms, bool allow_ksplit) {
+// epi: only the kinds whose epilogue runs beside the next chunk's MMAs (two
+// accumulators) and has the form with bias, activation and residual.
+PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms, bool allow_ksplit,
+                       bool epi = false) {
     struct Key {
         int64_t M, d_out, d_in, r;
         int sms;
-        bool ks;
+        bool ks, epi;
     };
     static std::mutex mu;
     static Key keys[64];
@@ -1923,13 +1994,14 @@ PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sm
         std::lock_guard<std::mutex> lock(mu);
         for (int i = 0; i < n_cached; ++i)
             if (keys[i].M == M && keys[i].d_out == d_out && keys[i].d_in == d_in && keys[i].r == r &&
-                keys[i].sms == sms && keys[i].ks == allow_ksplit)
+                keys[i].sms == sms && keys[i].ks == allow_ksplit && keys[i].epi == epi)
                 return vals[i];
     }
     const int maxp = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
     PlanChoice best{-1, 0, 1};
     double best_cost = 0;
     for (int kind = 0; kind < 4; ++kind) {
+        if (epi && kind >= 2) continue;
         if (kind == 0 && M >= 192) continue;   // 128-token chunks: below 192 tokens only
         const int cap = kind == 0 ? Cfg2<128>::CHU : kind == 3 ? Cfg2<256>::CHU : Cfg2<240>::CHU;
         const int half_n = cap * 8;
@@ -1949,7 +2021,7 @@ PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sm
         }
     }
     std::lock_guard<std::mutex> lock(mu);
-    keys[next_slot] = Key{M, d_out, d_in, r, sms, allow_ksplit};
+    keys[next_slot] = Key{M, d_out, d_in, r, sms, allow_ksplit, epi};
     vals[next_slot] = best;
     next_slot = (next_slot + 1) % 64;
     if (n_cached < 64) ++n_cached;
@@ -2026,13 +2098,12 @@ int64_t plan_check(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int kernel
     return bad;
 }
 
-template <int BN>
+template <int BN, bool kEpi = false>
 cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
                                uint16_t *Y, bool after_projection, int tail_mode, cudaStream_t stream, int chu = 0,
                                const Epilogue *ep = nullptr) {
-    using C = Cfg2<BN>;
-    const auto kernel = ep != nullptr ? tc2_forward_kernel<BN, true> : tc2_forward_kernel<BN, false>;
+    using C = Cfg2<BN, kEpi>;
     if (tail_mode == 2) tail_mode = 1;   // the K split is the 512-row kernel's
     Maps2 maps;
     memset(&maps, 0, sizeof maps);
@@ -2046,7 +2117,7 @@ cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *val
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t err = cudaFuncSetAttribute(tc2_forward_kernel<BN, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     Params2 prm;
     int pairs = 0;
@@ -2064,7 +2135,7 @@ cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *val
     // ordinary launch, which must not overlap an unrelated preceding kernel.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(kThreads2);
+    cfg.blockDim = dim3(kEpi ? kThreads2E : kThreads2);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -2072,17 +2143,28 @@ cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *val
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (after_projection && r > 0) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, prm, ep != nullptr ? *ep : Epilogue{});
+    if constexpr (kEpi) {
+        EpiArgs2 ea;
+        memset(&ea, 0, sizeof ea);
+        ea.ep = *ep;
+        if (ep->res != nullptr &&
+            !make_map(&ea.r16, kBF16, ep->res, d_out, M, ep->ldr * 2, BM, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+        if (ep->pre != nullptr &&
+            !make_map(&ea.z16, kBF16, ep->pre, d_out, M, d_out * 2, BM, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+        return cudaLaunchKernelEx(&cfg, tc2_forward_kernel<BN, true>, maps, prm, ea);
+    } else {
+        return cudaLaunchKernelEx(&cfg, tc2_forward_kernel<BN, false>, maps, prm, NoEpiArgs2{});
+    }
 }
 
 template <int BN>
 cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
                                uint16_t *Y, bool after_projection, int tail_mode, cudaStream_t stream, int chu = 0,
-                               const uint16_t *V = nullptr, uint8_t *fused_ws = nullptr, size_t ws_bytes = 0,
-                               const Epilogue *ep = nullptr) {
+                               const uint16_t *V = nullptr, uint8_t *fused_ws = nullptr, size_t ws_bytes = 0) {
     using C = CfgT<BN>;
-    const auto kernel = ep != nullptr ? tc2t_forward_kernel<BN, true> : tc2t_forward_kernel<BN, false>;
     // With a fused workspace (single-call forward, r > 0) T lives in its
     // first region; the kernel forms T itself (projection phase) when r <=
     // 128, and the last round may be split along K (partials and counters in
@@ -2106,7 +2188,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t err = cudaFuncSetAttribute(tc2t_forward_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     Params2 prm;
     int pairs = 0;
@@ -2122,7 +2204,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
         occ.gridDim = dim3((unsigned)(2 * max_pairs));
         occ.blockDim = dim3(kThreadsT);
         occ.dynamicSmemBytes = C::SMEM;
-        err = cudaOccupancyMaxActiveClusters(&ncl, kernel, &occ);
+        err = cudaOccupancyMaxActiveClusters(&ncl, tc2t_forward_kernel<BN>, &occ);
         if (err != cudaSuccess) return err;
         if (ncl < max_pairs) max_pairs = ncl;
         if (max_pairs < 1) return cudaErrorInvalidConfiguration;
@@ -2192,7 +2274,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (after_projection && r > 0 && !tp) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, prm, ep != nullptr ? *ep : Epilogue{});
+    return cudaLaunchKernelEx(&cfg, tc2t_forward_kernel<BN>, maps, prm);
 }
 
 
@@ -2557,13 +2639,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_base = *tmem_slot;
     }
 
-    uint32_t r2[2] = {0, 0};
+    // kEpi: the residual of the four items (row, four tokens) from `it` on that
+    // this thread reduces at the end.
+    uint32_t r2[kEpi ? 4 : 1][2];
+    auto load_res = [&](int it) {
+        const int rpc = BM / (int)ks_n;
+#pragma unroll
+        for (int b = 0; b < 4; ++b, it += 128)
+            if (it < rpc * (BN / 4))
+                load_res_row<4>(ep, tok0 + 4 * (it / rpc), M, d0 + (int)ks_q * rpc + it % rpc, d_out, r2[b]);
+    };
     if constexpr (kEpi) {
         if (warp >= 2 && ep.res != nullptr) {
             if (pdl == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
-            const int it = threadIdx.x - 64, rpc = BM / (int)ks_n;
-            if (it < rpc * (BN / 4))
-                load_res_row<4>(ep, tok0 + 4 * (it / rpc), M, d0 + (int)ks_q * rpc + it % rpc, d_out, r2);
+            load_res(threadIdx.x - 64);
         }
     }
 
@@ -2708,7 +2797,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int rpc = BM / (int)ks_n;
         const int items = rpc * (BN / 4);
         const uint32_t part_addr = smem_u32(part);
-        for (int it = threadIdx.x - 64; it < items; it += 128) {
+        auto reduce = [&](int it, [[maybe_unused]] const uint32_t *rr) {
             const int row = (int)ks_q * rpc + it % rpc;
             const int tg = it / rpc;
             const uint32_t off = (uint32_t)((row * C::PROW + 4 * tg) * 4);
@@ -2720,11 +2809,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                             p[0].z + p[1].z + p[2].z + p[3].z, p[0].w + p[1].w + p[2].w + p[3].w};
             const int out_row = d0 + row;
             if constexpr (kEpi) {
-                const int tq = tok0 + 4 * tg;
                 float bias = 0.f;
                 if (ep.bias != nullptr && out_row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + out_row));
-                if (it >= 128) load_res_row<4>(ep, tq, M, out_row, d_out, r2);
-                epilogue_row<4>(ep, sum, bias, r2, tq, M, out_row, d_out);
+                epilogue_row<4>(ep, sum, bias, rr, tok0 + 4 * tg, M, out_row, d_out);
             }
             if (out_row < d_out) {
 #pragma unroll
@@ -2733,6 +2820,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (tok < M) Y[(int64_t)tok * d_out + out_row] = f32_to_bf16_bits(sum[j]);
                 }
             }
+        };
+        if constexpr (kEpi) {
+            for (int it = threadIdx.x - 64; it < items; it += 512) {
+                if (it >= 512 && ep.res != nullptr) load_res(it);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (it + 128 * b < items) reduce(it + 128 * b, ep.res != nullptr ? r2[b] : nullptr);
+            }
+        } else {
+            for (int it = threadIdx.x - 64; it < items; it += 128) reduce(it, nullptr);
         }
     }
     cluster_sync_all();  // no CTA leaves while its partial may still be read
@@ -2744,12 +2841,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // pdl: 0 plain launch, 1 after the projection kernel (waits before T), 2
 // chained (waits before X and T).
-template <int BN>
+template <int BN, bool kEpi = false>
 cudaError_t launch_sparse_small(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                 int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
                                 uint16_t *Y, int pdl, cudaStream_t stream, const Epilogue *ep = nullptr) {
     using C = CfgS<BN>;
-    const auto kernel = ep != nullptr ? tc_small_kernel<BN, true> : tc_small_kernel<BN, false>;
+    const auto kernel = tc_small_kernel<BN, kEpi>;
     CUtensorMap m_vals, m_meta, m_x, m_u, m_t;
     memset(&m_u, 0, sizeof m_u);
     memset(&m_t, 0, sizeof m_t);
@@ -2790,6 +2887,35 @@ cudaError_t launch_sparse_small(const uint16_t *X, int64_t M, const uint16_t *va
                               ep != nullptr ? *ep : Epilogue{});
 }
 
+// The forward with bias, activation and residual: the split-K kernel where the
+// plain forward takes it, else the pair kernels with two accumulators, whose
+// epilogue runs beside the next chunk's MMAs.  The 512-row kernel has no room
+// for that (its accumulators are drained between chunks): on the 14336 x 4096
+// layer at 2048 tokens, where the plain forward takes it (121 us against 130),
+// a drain with tanh GELU took 304 us, the 256-row kernel's whole call 149.
+cudaError_t launch_epilogue(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta, int64_t d_out,
+                            int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r, uint16_t *Y, int pdl,
+                            const char *force, const Epilogue &ep, cudaStream_t stream) {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const bool f128 = force != nullptr && strncmp(force, "2sm128", 6) == 0;
+    const bool f240 = force != nullptr && strncmp(force, "2sm240", 6) == 0;
+    const bool fsmall = force != nullptr && strcmp(force, "small") == 0;
+    if (f128 || f240 || (!fsmall && M > kChainMaxM && !small_wins(M, d_out, d_in, sms))) {
+        PlanChoice c = choose_plan(M, d_out, d_in, r, sms, false, true);
+        if (f128 || f240) c = PlanChoice{f128 ? 0 : 1, 0, force[strlen(force) - 1] == 'w' ? 0 : 1};
+        if (c.kind == 0)
+            return launch_sparse_pair<128, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl == 1, c.tail, stream,
+                                                 c.chu, &ep);
+        return launch_sparse_pair<240, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl == 1, c.tail, stream, c.chu,
+                                             &ep);
+    }
+    if (M <= 16) return launch_sparse_small<16, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, &ep);
+    if (M <= 32) return launch_sparse_small<32, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, &ep);
+    if (M <= 64) return launch_sparse_small<64, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, &ep);
+    return launch_sparse_small<128, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, &ep);
+}
+
 }  // namespace tc
 
 cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
@@ -2804,23 +2930,24 @@ cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals
     // (a trailing w deals whole tiles only); used by the tests and for A/B
     // measurements.
     const char *force = getenv("SLR_TC_KERNEL");
+    if (ep != nullptr) return tc::launch_epilogue(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, force, *ep, stream);
     if (force != nullptr) {
-        if (strcmp(force, "1sm") == 0 && ep == nullptr) return tc::launch_sparse<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, stream);
+        if (strcmp(force, "1sm") == 0) return tc::launch_sparse<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, stream);
         const bool whole = force[0] != 0 && force[strlen(force) - 1] == 'w';
         const int tail = whole ? 0 : 1;
         if (strncmp(force, "2sm128", 6) == 0)
-            return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, ep);
+            return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
         if (strncmp(force, "2sm256", 6) == 0)
-            return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, ep);
+            return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
         if (strncmp(force, "2sm240", 6) == 0)
-            return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, ep);
+            return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
         if (strncmp(force, "2smtall", 7) == 0)
-            return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream, 0, nullptr, nullptr, 0, ep);
+            return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, tail, stream);
         if (strcmp(force, "small") == 0) {
-            if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
-            if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
-            if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
-            return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+            if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+            if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+            if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+            return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
         }
     }
     // Up to 64 tokens the layer streams S: the split-K kernel.  Above, the
@@ -2831,21 +2958,21 @@ cudaError_t launch_tc_forward(const uint16_t *X, int64_t M, const uint16_t *vals
     // chunks; each with the last round split among all pairs or dealt as whole
     // tiles.  The pair plan with the smallest estimated time of its slowest
     // pair is launched.
-    if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
-    if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
-    if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+    if (M <= 16) return tc::launch_sparse_small<16>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+    if (M <= 32) return tc::launch_sparse_small<32>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
+    if (M <= 64) return tc::launch_sparse_small<64>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (tc::small_wins(M, d_out, d_in, sms))
-        return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream, ep);
+        return tc::launch_sparse_small<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl, stream);
     const tc::PlanChoice c = tc::choose_plan(M, d_out, d_in, r, sms, false);
     if (c.kind == 0)
-        return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, ep);
+        return tc::launch_sparse_pair<128>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
     if (c.kind == 1)
-        return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, ep);
+        return tc::launch_sparse_pair<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
     if (c.kind == 3)
-        return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, ep);
-    return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu, nullptr, nullptr, 0, ep);
+        return tc::launch_sparse_pair<256>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
+    return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, after_projection, c.tail, stream, c.chu);
 }
 
 cudaError_t launch_tc_forward_fused(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
@@ -2863,7 +2990,7 @@ cudaError_t launch_tc_forward_fused(const uint16_t *X, int64_t M, const uint16_t
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const char *force = getenv("SLR_TC_KERNEL");
-    if (r > 0) {
+    if (r > 0 && ep == nullptr) {
         if (force != nullptr) {
             if (strncmp(force, "2smtall", 7) == 0) {
                 const char last = force[strlen(force) - 1];
@@ -2879,7 +3006,7 @@ cudaError_t launch_tc_forward_fused(const uint16_t *X, int64_t M, const uint16_t
     }
     if (tail >= 0)
         return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, false, tail, stream, chu, V,
-                                           ws, ws_bytes, ep);
+                                           ws, ws_bytes);
     cudaError_t err = cudaSuccess;
     if (r > 0) err = launch_tc_project(X, M, V, d_in, r, T16, false, stream);
     if (err == cudaSuccess) err = launch_tc_forward(X, M, vals, meta, d_out, d_in, U, r > 0 ? T16 : nullptr, r, Y, 1, stream, ep);

@@ -73,7 +73,8 @@ def test_forward_epilogue_argument_errors():
     assert _fwd(flags=2) == ARG and _fwd(path=9) == ARG
     assert _fwd(ldr=255) == SHAPE
     assert _fwd(R=0x6000, ldr=264) == SHAPE        # Y itself as residual has Y's rows
-    assert _fwd(bias=0x8001) == ALIGN and _fwd(R=0x9001) == ALIGN and _fwd(Z=0xa001) == ALIGN
+    assert _fwd(bias=0x8001) == ALIGN and _fwd(R=0x9002) == ALIGN and _fwd(Z=0xa008) == ALIGN
+    assert _fwd(ldr=260) == SHAPE                  # the tensor-core path's rows of R are 16-byte aligned
     assert _fwd(X=0) == NULL and _fwd(Y=0) == NULL and _fwd(U=0) == NULL and _fwd(ws=0) == NULL
     assert _fwd(d_in=200) == SHAPE and _fwd(r=12) == SHAPE and _fwd(d_out=100, ldr=100, path=2) == SHAPE
     assert _fwd(Y=0x6008) == ALIGN and _fwd(ws_bytes=16) == WORKSPACE
@@ -81,7 +82,8 @@ def test_forward_epilogue_argument_errors():
         assert _fwd() == DEVICE
         assert _fwd(bias=0, R=0, ldr=0, Z=0, act=0) == DEVICE
         assert _fwd(R=0x6000, ldr=256) == DEVICE   # in place
-        assert _fwd(bias=0x8002, R=0x9002, Z=0xa002) == DEVICE
+        assert _fwd(bias=0x8002) == DEVICE
+        assert _fwd(M=1, ldr=260) == DEVICE and _fwd(ldr=259, path=1) == DEVICE   # one row; the streaming path
 
 
 def test_binding_refuses_host_tensors_and_unknown_activations():

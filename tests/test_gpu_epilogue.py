@@ -98,11 +98,11 @@ def test_epilogue_operands(M, act, bias, res):
     run(Layer(M, 272, 256, 16, M, ldr=280), act, bias, res, pre=M != 9)
 
 
-@pytest.mark.parametrize("kernel", ["small", "2sm128", "2sm240", "2sm240w", "2sm256", "2smtall", "2smtallw", "2smtallk"])
+@pytest.mark.parametrize("kernel", ["small", "2sm128", "2sm240", "2sm240w"])
 @pytest.mark.parametrize("M,d_out,d_in,r", [(70, 520, 256, 16), (250, 1032, 640, 64), (500, 2056, 2048, 72)])
 def test_epilogue_kernels(kernel, M, d_out, d_in, r, monkeypatch):
     monkeypatch.setenv("SLR_TC_KERNEL", kernel)
-    run(Layer(M, d_out, d_in, r, M + r, ldr=d_out + 13), "gelu_tanh", True, True, True, path="tensor")
+    run(Layer(M, d_out, d_in, r, M + r, ldr=d_out + 24), "gelu_tanh", True, True, True, path="tensor")
 
 
 @pytest.mark.parametrize("M,path", [(1, "decode"), (5, "tensor"), (64, "tensor"), (5, "decode"), (129, "tensor"),
