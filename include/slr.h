@@ -434,6 +434,32 @@ SLR_API slr_status slr_forward_epilogue(const void *X, int64_t M, const void *va
                                         slr_act act, const void *R, int64_t ldr, void *Z, void *Y, void *workspace,
                                         size_t workspace_bytes, slr_path path, uint32_t flags, slr_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Gradient through the epilogue of slr_forward_epilogue.
+ *
+ *        dZ = dY * act'(Z)        db_j = sum_m dZ[m][j]
+ *
+ * for an upstream gradient dY of Y = act(Z) + R.  dZ is what
+ * slr_lora_backward and slr_input_backward take as their dY; the residual's
+ * gradient is dY itself.
+ *
+ *   dY   device, bf16 [M, d_out], read only unless dZ is dY.
+ *   Z    device, bf16 [M, d_out]: the pre-activation from the forward; not
+ *        looked at for SLR_ACT_NONE.
+ *   dZ   device, bf16 [M, d_out], out, or NULL.  May be dY or Z itself.
+ *   db   device, fp32 [d_out], out, or NULL (not both).
+ *
+ * relu's slope is 1 for Z > 0, else 0; at infinite Z the slopes of the others
+ * are their limits; NaN gives NaN.  The products are fp32 and rounded to bf16
+ * once; db adds them unrounded, in fp32 (a thread's sums of at most 64 rows
+ * first), in a fixed order: results are deterministic.
+ *
+ * Requirements: M >= 0 (M == 0 zeroes db), d_out >= 8 with d_out % 8 == 0, M,
+ * d_out < 2^31; all pointers 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+SLR_API slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t M, int64_t d_out, slr_act act,
+                                         void *dZ, float *db, slr_stream_t stream);
+
 /* The two stages of slr_forward, for callers that schedule or time them
  * separately.  slr_forward(...) == slr_forward_project(...) followed on the same
  * stream by slr_forward_combine(...) with the same path and workspace.

@@ -19,6 +19,7 @@ Functions mirror the C ABI in ``include/slr.h``:
   ``slr_forward_with_path`` / ``slr_forward_ex``
 * ``forward_epilogue(X, vals, meta, U, V, bias, act, residual) -> Y``  --
   ``slr_forward_epilogue``
+* ``epilogue_backward(dY, Z, act) -> (dZ, dbias)``  -- ``slr_epilogue_backward``
 * ``workspace_size``, ``select_path``, ``check_kernel_error``
 
 Tensors are torch CUDA tensors (torch only provides memory and the current
@@ -93,6 +94,8 @@ def _load() -> ctypes.CDLL:
     lib.slr_forward_epilogue.restype = st
     lib.slr_forward_epilogue.argtypes = [p, i64, p, p, i64, i64, p, p, i64, p, st, p, i64, p, p, p, sz, st,
                                          ctypes.c_uint32, p]
+    lib.slr_epilogue_backward.restype = st
+    lib.slr_epilogue_backward.argtypes = [p, p, i64, i64, st, p, p, p]
     lib.slr_forward_workspace_size.restype = sz
     lib.slr_forward_workspace_size.argtypes = [i64, i64, i64, i64]
     lib.slr_forward_select_path.restype = st
@@ -420,6 +423,34 @@ def forward_epilogue(X: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, U:
                                      FWD_OVERLAP_PRECEDING if overlap_preceding else 0, stream),
            "slr_forward_epilogue")
     return out
+
+
+def epilogue_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str, *, want_dbias: bool = True,
+                      out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """``(dZ, dbias)`` of :func:`forward_epilogue` for upstream ``dY`` [M, d_out]
+    (``slr_epilogue_backward``): ``dZ = dY * act'(Z)`` (bf16) and its column
+    sums (fp32 [d_out]; None unless ``want_dbias``).  ``out`` receives dZ and
+    may be ``dY`` or ``Z``.  Without an activation the gradient passes
+    unchanged: ``dY`` itself is returned when no ``out`` is given."""
+    if dY.dim() != 2 or act not in ACTS:
+        raise ValueError(f"dY must be 2-D and act one of {', '.join(ACTS)}")
+    device, stream = _current(dY)
+    shape = dY.shape
+    _expect("dY", dY, torch.bfloat16, shape, device)
+    if act != "none":
+        if Z is None:
+            raise ValueError("an activation's gradient needs the pre-activation Z")
+        _expect("Z", Z, torch.bfloat16, shape, device)
+    if out is not None:
+        _expect("out", out, torch.bfloat16, shape, device)
+    elif act != "none":
+        out = torch.empty_like(dY)
+    elif not want_dbias:
+        return dY, None
+    dbias = torch.empty(shape[1], dtype=torch.float32, device=device) if want_dbias else None
+    _check(_lib.slr_epilogue_backward(dY.data_ptr(), _addr(Z) if act != "none" else None, shape[0], shape[1], ACTS[act],
+                                      _addr(out), _addr(dbias), stream), "slr_epilogue_backward")
+    return (dY if out is None else out), dbias
 
 
 def forward_project(X: torch.Tensor, V: torch.Tensor | None, d_out: int, workspace: torch.Tensor, *,

@@ -502,4 +502,24 @@ slr_status slr_forward_epilogue(const void *X, int64_t M, const void *vals, cons
                              reinterpret_cast<cudaStream_t>(stream), plain ? nullptr : &ep);
 }
 
+slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t M, int64_t d_out, slr_act act, void *dZ,
+                                 float *db, slr_stream_t stream) {
+    if (!slr::act_ok(act)) return SLR_ERR_ARG;
+    if (dZ == nullptr && db == nullptr) return SLR_ERR_NULL;
+    if (M > 0 && (dY == nullptr || (act != SLR_ACT_NONE && Z == nullptr))) return SLR_ERR_NULL;
+    if (M < 0 || d_out < 8 || d_out % 8 != 0 || M > INT32_MAX || d_out > INT32_MAX) return SLR_ERR_SHAPE;
+    if (!slr::aligned16(dY) || !slr::aligned16(Z) || !slr::aligned16(dZ) || !slr::aligned16(db)) return SLR_ERR_ALIGN;
+    const slr_status dev = slr::check_device();
+    if (dev != SLR_OK) return dev;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
+    if (M == 0) {
+        if (db != nullptr) err = cudaMemsetAsync(db, 0, (size_t)d_out * sizeof(float), st);
+    } else {
+        err = slr::launch_epilogue_backward(static_cast<const uint16_t *>(dY), static_cast<const uint16_t *>(Z), M, d_out,
+                                            (int)act, static_cast<uint16_t *>(dZ), db, st);
+    }
+    return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
+}
+
 }  // extern "C"

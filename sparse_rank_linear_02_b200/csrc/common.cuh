@@ -150,4 +150,9 @@ cudaError_t launch_decode_forward(const uint16_t *X, int64_t M, const uint16_t *
                                   const uint16_t *U, const float *T32, int64_t r, uint16_t *Y,
                                   int pdl_mode, cudaStream_t stream, const Epilogue *ep = nullptr);
 
+// dZ = dY * act'(Z) and db = its fp32 column sums (dZ or db may be null; dZ may
+// be dY or Z).  d_out % 8 == 0, 16-byte aligned pointers, M >= 1.
+cudaError_t launch_epilogue_backward(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t d_out, int act,
+                                     uint16_t *dZ, float *db, cudaStream_t stream);
+
 }  // namespace slr

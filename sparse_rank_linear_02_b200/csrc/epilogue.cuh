@@ -6,12 +6,18 @@
 //
 // The activations, with u = sqrt(2/pi) (z + 0.044715 z^3):
 //   relu       max(z, 0)                        slope [z > 0]
-//   gelu       z Phi(z) = z erfc(-z/sqrt 2)/2   slope Phi(z) + z phi(z)
+//   gelu       z Phi(z)                         slope Phi(z) + z phi(z)
 //   gelu_tanh  z (1 + tanh u)/2 = z / (1 + e^-2u)
 //   silu       z / (1 + e^-z)
 // The quotient forms have no cancellation for negative z, where 1 + tanh u
-// would lose every digit; erfc serves the Gaussian distribution function for
-// the same reason.  NaN stays NaN in every one of them.
+// would lose every digit.  NaN stays NaN in every one of them.
+//
+// Phi: for a >= 0 the tail 1 - Phi(a) is e^(-a^2/2) times a smooth function of
+// t = 1 / (1 + 0.35 a), here t times a polynomial of degree 8 in t, fitted to
+// the least largest relative error (3.2e-8 for a <= 13.5).  It costs one
+// reciprocal, one exponential and ten multiply-adds, shares the exponential
+// with the slope's density, and keeps the tail's relative accuracy; erfcf took
+// 160 us where this takes the tanh form's 134 (14336 x 4096, 2048 tokens).
 #pragma once
 
 #include "common.cuh"
@@ -28,15 +34,82 @@ struct Epilogue {
 };
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
-constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-__device__ __forceinline__ float act_gelu(float z) { return 0.5f * z * erfcf(-z * kInvSqrt2); }
+// Phi(z), given e = exp(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+    const float t = __fdividef(1.0f, fmaf(0.35f, fabsf(z), 1.0f));
+    float q = -0.029125869274139404f;
+    q = fmaf(q, t, 0.1438722461462021f);
+    q = fmaf(q, t, -0.2555046081542969f);
+    q = fmaf(q, t, 0.15892933309078217f);
+    q = fmaf(q, t, -0.022937165573239326f);
+    q = fmaf(q, t, 0.10543294996023178f);
+    q = fmaf(q, t, 0.11985243111848831f);
+    q = fmaf(q, t, 0.13985908031463623f);
+    q = fmaf(q, t, 0.1396215707063675f);
+    const float tail = q * t * e;
+    return z < 0.f ? tail : 1.0f - tail;
+}
+
+__device__ __forceinline__ float act_gelu(float z) { return z * normal_cdf(z, __expf(-0.5f * z * z)); }
 __device__ __forceinline__ float act_gelu_tanh(float z) {
     const float u = kGeluC * fmaf(0.044715f * z, z * z, z);
     return __fdividef(z, 1.0f + __expf(-2.0f * u));
 }
 __device__ __forceinline__ float act_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// z within [-c, c], NaN kept.  The slopes are at their limits, 0 and 1, well
+// inside the bounds used below, where no product of a zero and an infinity
+// arises.
+__device__ __forceinline__ float clamp_keep_nan(float z, float c) {
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(z), "f"(-c), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float slope_gelu(float z) {
+    z = clamp_keep_nan(z, 40.f);
+    const float e = __expf(-0.5f * z * z);
+    return fmaf(z * kInvSqrt2Pi, e, normal_cdf(z, e));
+}
+__device__ __forceinline__ float slope_gelu_tanh(float z) {
+    z = clamp_keep_nan(z, 40.f);
+    const float z2 = z * z;
+    const float s = __fdividef(1.0f, 1.0f + __expf(-2.0f * kGeluC * fmaf(0.044715f * z, z2, z)));
+    return fmaf(z * s * (1.0f - s), 2.0f * kGeluC * fmaf(0.134145f, z2, 1.0f), s);
+}
+__device__ __forceinline__ float slope_silu(float z) {
+    z = clamp_keep_nan(z, 200.f);
+    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+    return s * fmaf(z, 1.0f - s, 1.0f);
+}
+
+// z becomes act'(z) over N values.
+template <int N>
+__device__ __forceinline__ void slope_values(float (&z)[N], int act) {
+    switch (act) {
+        case SLR_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = z[i] > 0.f ? 1.f : 0.f;
+            break;
+        case SLR_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = slope_gelu(z[i]);
+            break;
+        case SLR_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = slope_gelu_tanh(z[i]);
+            break;
+        case SLR_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = slope_silu(z[i]);
+            break;
+        default:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = 1.f;
+            break;
+    }
+}
 
 // act over N values; the switch is uniform and outside the loops.
 template <int N>

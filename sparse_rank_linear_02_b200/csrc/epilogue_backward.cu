@@ -1,0 +1,152 @@
+// epilogue_backward.cu -- gradient through the layer's bias and activation.
+//
+//   dZ = dY * act'(Z)        db_j = sum over the tokens m of dZ[m][j]
+//
+// for Y = act(Z) + R, Z = X S^T + T U^T + b: one pass over dY and Z.  The sums
+// take the fp32 products before their rounding to bf16.
+//
+// Bound by HBM: 6 bytes per element.  A cluster of KS <= 8 CTAs owns a strip of
+// 8 * LANES columns and splits its tokens, so one launch also finishes db: the
+// CTAs' column sums meet through distributed shared memory and are added in
+// CTA order (the result does not depend on timing).  LANES threads read a row
+// of the strip, 16 bytes each; a thread has four rows of both inputs in flight.
+// A thread's sums go through two levels (at most 64 rows, then the sums of
+// those), which bounds the rounding for long batches.
+#include "common.cuh"
+#include "epilogue.cuh"
+#include "tc_ptx.cuh"
+
+namespace slr {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+constexpr int kFold = 64 / kUnroll;   // passes between folds of the first level
+
+// Coherent loads: dZ may be dY or Z itself.
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+template <int LANES>
+__global__ void __launch_bounds__(kThreads, 4)
+    epilogue_backward_kernel(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t d_out, int act, uint16_t *dZ,
+                             float *db) {
+    constexpr int kRows = kThreads / LANES;   // rows of one pass
+    __shared__ float red[kRows][8 * LANES + 4];
+    __shared__ float cols[8 * LANES];
+    uint32_t ks_n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ks_n));
+    const uint32_t ks_q = tc::cluster_ctarank();
+    const int64_t strip = blockIdx.x / ks_n;
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const int64_t col = (strip * LANES + lane) * 8;
+    const int64_t m1 = M * (ks_q + 1) / ks_n;
+    float part[8];
+    float *own = &red[sub][8 * lane];   // second level of this thread's sums
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i] = part[i] = 0.f;
+    if (col < d_out) {
+        int pass = 0;
+        const int64_t step = (int64_t)kRows * d_out, end = m1 * d_out;
+        for (int64_t at = (M * ks_q / ks_n + sub) * d_out + col; at < end; at += kUnroll * step) {
+            uint4 g[kUnroll], z[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (at + u * step < end) {
+                    g[u] = ld_v4(dY + at + u * step);
+                    if (act != SLR_ACT_NONE) z[u] = ld_v4(Z + at + u * step);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (at + u * step >= end) break;
+                const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+                const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
+                float v[8];
+                uint32_t o[4];
+                if (act != SLR_ACT_NONE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = (i & 1) ? bf16hi_to_f32(zw[i / 2]) : bf16lo_to_f32(zw[i / 2]);
+                }
+                slope_values<8>(v, act);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] *= (i & 1) ? bf16hi_to_f32(gw[i / 2]) : bf16lo_to_f32(gw[i / 2]);
+                    part[i] += v[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = (uint32_t)f32_to_bf16_bits(v[2 * i]) | ((uint32_t)f32_to_bf16_bits(v[2 * i + 1]) << 16);
+                if (dZ != nullptr) *reinterpret_cast<uint4 *>(dZ + at + u * step) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if (++pass == kFold) {
+                pass = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    own[i] += part[i];
+                    part[i] = 0.f;
+                }
+            }
+        }
+    }
+    if (db == nullptr) return;   // uniform over the grid
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i] += part[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 8 * LANES; c += kThreads) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < kRows; ++r) s += red[r][c];
+        cols[c] = s;
+    }
+    tc::cluster_sync_all();   // every CTA's column sums are in its shared memory
+    if (ks_q == 0) {
+        const uint32_t base = tc::smem_u32(cols);
+        for (int c = threadIdx.x; c < 8 * LANES; c += kThreads) {
+            float s = 0.f;
+            for (uint32_t q = 0; q < ks_n; ++q) {
+                float v;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::mapa_shared(base + 4 * c, q)));
+                s += v;
+            }
+            if (strip * LANES * 8 + c < d_out) db[strip * LANES * 8 + c] = s;
+        }
+    }
+    tc::cluster_sync_all();   // no CTA leaves while its sums may still be read
+}
+
+template <int LANES>
+cudaError_t launch_lanes(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t d_out, int act, uint16_t *dZ,
+                         float *db, cudaStream_t stream) {
+    const int64_t strips = (d_out + 8 * LANES - 1) / (8 * LANES);
+    unsigned ks = 1;
+    while (ks < 8 && M > (int64_t)ks * (kThreads / LANES) * kUnroll) ks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(strips * ks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, epilogue_backward_kernel<LANES>, dY, Z, M, d_out, act, dZ, db);
+}
+
+}  // namespace
+
+cudaError_t launch_epilogue_backward(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t d_out, int act,
+                                     uint16_t *dZ, float *db, cudaStream_t stream) {
+    if (d_out >= 8192) return launch_lanes<32>(dY, Z, M, d_out, act, dZ, db, stream);
+    if (d_out >= 2048) return launch_lanes<16>(dY, Z, M, d_out, act, dZ, db, stream);
+    return launch_lanes<8>(dY, Z, M, d_out, act, dZ, db, stream);
+}
+
+}  // namespace slr

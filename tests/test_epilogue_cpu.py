@@ -93,3 +93,19 @@ def test_binding_refuses_host_tensors_and_unknown_activations():
         slr.forward_epilogue(X, vals, meta, None, None, act="swish")
     with pytest.raises(ValueError, match="CUDA device"):
         slr.forward_epilogue(X, vals, meta, None, None)
+
+
+def test_epilogue_backward_argument_errors():
+    f = slr.lib().slr_epilogue_backward
+    dy, z, dz, db = (P(0x10000 * k) for k in range(1, 5))
+    assert f(dy, z, 8, 16, 5, dz, db, None) == ARG
+    assert f(dy, z, 8, 16, 2, None, None, None) == NULL
+    assert f(None, z, 8, 16, 2, dz, db, None) == NULL
+    assert f(dy, None, 8, 16, 2, dz, db, None) == NULL
+    assert f(dy, z, 8, 12, 2, dz, db, None) == SHAPE and f(dy, z, -1, 16, 2, dz, db, None) == SHAPE
+    assert f(dy, z, 8, 0, 2, dz, db, None) == SHAPE and f(dy, z, 1 << 31, 16, 2, dz, db, None) == SHAPE
+    assert f(P(0x10008), z, 8, 16, 2, dz, db, None) == ALIGN and f(dy, P(0x20002), 8, 16, 2, dz, db, None) == ALIGN
+    assert f(dy, z, 8, 16, 2, P(0x30008), db, None) == ALIGN and f(dy, z, 8, 16, 2, dz, P(0x40004), None) == ALIGN
+    if not torch.cuda.is_available():
+        assert f(dy, z, 8, 16, 2, dz, None, None) == DEVICE and f(dy, None, 8, 16, 0, None, db, None) == DEVICE
+        assert f(None, None, 0, 16, 2, None, db, None) == DEVICE
