@@ -36,101 +36,131 @@ struct Epilogue {
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// Phi(z), given e = exp(-z^2 / 2).
-__device__ __forceinline__ float normal_cdf(float z, float e) {
-    const float t = __fdividef(1.0f, fmaf(0.35f, fabsf(z), 1.0f));
-    float q = -0.029125869274139404f;
-    q = fmaf(q, t, 0.1438722461462021f);
-    q = fmaf(q, t, -0.2555046081542969f);
-    q = fmaf(q, t, 0.15892933309078217f);
-    q = fmaf(q, t, -0.022937165573239326f);
-    q = fmaf(q, t, 0.10543294996023178f);
-    q = fmaf(q, t, 0.11985243111848831f);
-    q = fmaf(q, t, 0.13985908031463623f);
-    q = fmaf(q, t, 0.1396215707063675f);
-    const float tail = q * t * e;
-    return z < 0.f ? tail : 1.0f - tail;
-}
-
-__device__ __forceinline__ float act_gelu(float z) { return z * normal_cdf(z, __expf(-0.5f * z * z)); }
-__device__ __forceinline__ float act_gelu_tanh(float z) {
-    const float u = kGeluC * fmaf(0.044715f * z, z * z, z);
-    return __fdividef(z, 1.0f + __expf(-2.0f * u));
-}
-__device__ __forceinline__ float act_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-
-// z within [-c, c], NaN kept.  The slopes are at their limits, 0 and 1, well
-// inside the bounds used below, where no product of a zero and an infinity
-// arises.
-__device__ __forceinline__ float clamp_keep_nan(float z, float c) {
-    float r;
-    asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(z), "f"(-c), "f"(c));
+// Two fp32 values in one register pair: the arithmetic below runs on
+// fma.rn.f32x2 and its kin, one issue slot for two results.  Written one value
+// at a time, the slopes bound the backward kernel by instruction issue.
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ float slope_gelu(float z) {
-    z = clamp_keep_nan(z, 40.f);
-    const float e = __expf(-0.5f * z * z);
-    return fmaf(z * kInvSqrt2Pi, e, normal_cdf(z, e));
+__device__ __forceinline__ f32x2 dup2(float a) { return pack2(a, a); }
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
-__device__ __forceinline__ float slope_gelu_tanh(float z) {
-    z = clamp_keep_nan(z, 40.f);
-    const float z2 = z * z;
-    const float s = __fdividef(1.0f, 1.0f + __expf(-2.0f * kGeluC * fmaf(0.044715f * z, z2, z)));
-    return fmaf(z * s * (1.0f - s), 2.0f * kGeluC * fmaf(0.134145f, z2, 1.0f), s);
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
-__device__ __forceinline__ float slope_silu(float z) {
-    z = clamp_keep_nan(z, 200.f);
-    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-    return s * fmaf(z, 1.0f - s, 1.0f);
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// 2^a and 1/a of both values: one special-function operation each.
+__device__ __forceinline__ f32x2 exp2_2(f32x2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return pack2(a, b);
+}
+__device__ __forceinline__ f32x2 rcp2(f32x2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return pack2(a, b);
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Phi(z), given e = exp(-z^2 / 2).
+__device__ __forceinline__ f32x2 normal_cdf2(f32x2 z, f32x2 e) {
+    float a, b;
+    unpack2(z, a, b);
+    const f32x2 t = rcp2(fma2(dup2(0.35f), pack2(fabsf(a), fabsf(b)), dup2(1.0f)));
+    f32x2 q = dup2(-0.029125869274139404f);
+    q = fma2(q, t, dup2(0.1438722461462021f));
+    q = fma2(q, t, dup2(-0.2555046081542969f));
+    q = fma2(q, t, dup2(0.15892933309078217f));
+    q = fma2(q, t, dup2(-0.022937165573239326f));
+    q = fma2(q, t, dup2(0.10543294996023178f));
+    q = fma2(q, t, dup2(0.11985243111848831f));
+    q = fma2(q, t, dup2(0.13985908031463623f));
+    q = fma2(q, t, dup2(0.1396215707063675f));
+    float ta, tb;
+    unpack2(mul2(mul2(q, t), e), ta, tb);
+    return pack2(a < 0.f ? ta : 1.0f - ta, b < 0.f ? tb : 1.0f - tb);
+}
+// exp(-z^2 / 2); 1 / (1 + exp(-2u)), u the tanh form's argument, z2 = z^2; 1 / (1 + exp(-z)).
+__device__ __forceinline__ f32x2 gauss2(f32x2 z) { return exp2_2(mul2(mul2(z, dup2(-0.5f * kLog2e)), z)); }
+__device__ __forceinline__ f32x2 sigma_tanh2(f32x2 z, f32x2 z2) {
+    const f32x2 w = mul2(fma2(dup2(-2.0f * kGeluC * kLog2e * 0.044715f), z2, dup2(-2.0f * kGeluC * kLog2e)), z);
+    return rcp2(add2(exp2_2(w), dup2(1.0f)));
+}
+__device__ __forceinline__ f32x2 sigma2(f32x2 z) { return rcp2(add2(exp2_2(mul2(z, dup2(-kLog2e))), dup2(1.0f))); }
+
+// act(z) of two values (not SLR_ACT_NONE).
+template <int ACT>
+__device__ __forceinline__ f32x2 act2(f32x2 z) {
+    if constexpr (ACT == SLR_ACT_GELU) return mul2(z, normal_cdf2(z, gauss2(z)));
+    if constexpr (ACT == SLR_ACT_GELU_TANH) return mul2(z, sigma_tanh2(z, mul2(z, z)));
+    if constexpr (ACT == SLR_ACT_SILU) return mul2(z, sigma2(z));
+    float a, b;
+    unpack2(z, a, b);
+    return pack2(a <= 0.f ? 0.f : a, b <= 0.f ? 0.f : b);
 }
 
-// z becomes act'(z) over N values.
-template <int N>
-__device__ __forceinline__ void slope_values(float (&z)[N], int act) {
-    switch (act) {
-        case SLR_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = z[i] > 0.f ? 1.f : 0.f;
-            break;
-        case SLR_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = slope_gelu(z[i]);
-            break;
-        case SLR_ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = slope_gelu_tanh(z[i]);
-            break;
-        case SLR_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = slope_silu(z[i]);
-            break;
-        default:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = 1.f;
-            break;
+// act'(z) of two values; |z| <= 200, where every slope is at its limit.
+template <int ACT>
+__device__ __forceinline__ f32x2 slope2(f32x2 z) {
+    const f32x2 neg = dup2(-1.0f);
+    if constexpr (ACT == SLR_ACT_GELU) {
+        const f32x2 e = gauss2(z);
+        return fma2(mul2(z, dup2(kInvSqrt2Pi)), e, normal_cdf2(z, e));
     }
+    if constexpr (ACT == SLR_ACT_GELU_TANH) {
+        const f32x2 z2 = mul2(z, z), s = sigma_tanh2(z, z2), p = mul2(z, s);
+        const f32x2 w = fma2(mul2(p, neg), s, p);   // z s (1 - s)
+        return fma2(w, fma2(dup2(2.0f * kGeluC * 0.134145f), z2, dup2(2.0f * kGeluC)), s);
+    }
+    if constexpr (ACT == SLR_ACT_SILU) {
+        const f32x2 s = sigma2(z), p = mul2(z, s);
+        return add2(s, fma2(mul2(p, neg), s, p));
+    }
+    if constexpr (ACT == SLR_ACT_RELU) {
+        float a, b;
+        unpack2(z, a, b);
+        return pack2(a > 0.f ? 1.f : 0.f, b > 0.f ? 1.f : 0.f);
+    }
+    return dup2(1.0f);
 }
 
 // act over N values; the switch is uniform and outside the loops.
+template <int ACT, int N>
+__device__ __forceinline__ void act_values_of(float (&z)[N]) {
+    if constexpr (N == 1) {
+        float unused;
+        unpack2(act2<ACT>(dup2(z[0])), z[0], unused);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) unpack2(act2<ACT>(pack2(z[i], z[i + 1])), z[i], z[i + 1]);
+    }
+}
 template <int N>
 __device__ __forceinline__ void act_values(float (&z)[N], int act) {
     switch (act) {
-        case SLR_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = z[i] <= 0.f ? 0.f : z[i];
-            break;
-        case SLR_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = act_gelu(z[i]);
-            break;
-        case SLR_ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = act_gelu_tanh(z[i]);
-            break;
-        case SLR_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = act_silu(z[i]);
-            break;
+        case SLR_ACT_RELU: act_values_of<SLR_ACT_RELU>(z); break;
+        case SLR_ACT_GELU: act_values_of<SLR_ACT_GELU>(z); break;
+        case SLR_ACT_GELU_TANH: act_values_of<SLR_ACT_GELU_TANH>(z); break;
+        case SLR_ACT_SILU: act_values_of<SLR_ACT_SILU>(z); break;
         default: break;
     }
 }
