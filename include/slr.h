@@ -460,6 +460,58 @@ SLR_API slr_status slr_forward_epilogue(const void *X, int64_t M, const void *va
 SLR_API slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t M, int64_t d_out, slr_act act,
                                          void *dZ, float *db, slr_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Distillation of a student's logits from a teacher's top logits.
+ *
+ * The recovery of a compressed model trains against the dense one (LoSparse
+ * combines its pruning with knowledge distillation); the teacher's largest
+ * logits per token, gathered once, stand for its distribution.  For token m
+ * with student logits z (n_vocab of them) and teacher entries (column i_j,
+ * logit t_j), j < k, at temperature tau:
+ *
+ *     p_j = exp(t_j / tau) / sum_j exp(t_j / tau)      q = softmax(z / tau)
+ *     loss[m] = tau^2 sum_j p_j (log p_j - log q[i_j])
+ *     dz[m][v] = dloss[m] tau (q[v] - sum of p_j with i_j == v)
+ *
+ * An entry whose column is outside [0, n_vocab) or whose logit is -inf is not
+ * there (a shorter list, or a padded token: all columns -1).  A token without
+ * entries has loss 0, lse 0 and a zero gradient whatever its logits hold; a
+ * token with dloss 0 has a zero gradient whatever its logits hold.  A column
+ * listed more than once counts with the sum of its p.  A -inf student logit has
+ * q = 0 (its listed p makes the loss +inf); NaN and +inf logits give NaN.
+ *
+ *   logits   device, bf16 [M, ldz] (ldz >= n_vocab).
+ *   idx      device, int32 [M, k];   teacher  device, fp32 [M, k].
+ *   loss     device, fp32 [M], out.
+ *   lse      device, fp32 [M]: log sum exp(z / tau), out of the forward (or
+ *            NULL there) and into the backward.
+ *   dloss    device, fp32 [M]: the upstream gradient of each token's loss, e.g.
+ *            its weight in the mean.
+ *   dlogits  device, bf16 [M, lddz] (lddz >= n_vocab), out.  May be logits
+ *            itself with lddz == ldz.
+ *
+ * slr_distill_forward gives loss and lse, slr_distill_backward the gradient
+ * from the forward's lse, slr_distill_loss_grad loss and gradient in one pass
+ * over the logits (where the weights are known beforehand: 4 bytes moved per
+ * logit instead of 6).  fp32 arithmetic, dlogits rounded to bf16 once;
+ * deterministic.
+ *
+ * Requirements: 0 <= M < 2^27 (M == 0 does nothing), 1 <= n_vocab < 2^31,
+ * 1 <= k <= SLR_DISTILL_MAX_K, 1e-4 <= tau <= 1e4 (SLR_ERR_ARG); logits and
+ * dlogits 2-byte aligned, the others 4-byte aligned.  Columns past n_vocab of
+ * a padded row are neither read nor written.
+ * ------------------------------------------------------------------------ */
+#define SLR_DISTILL_MAX_K 1024
+SLR_API slr_status slr_distill_forward(const void *logits, int64_t M, int64_t n_vocab, int64_t ldz, const int32_t *idx,
+                                       const float *teacher, int64_t k, float tau, float *loss, float *lse,
+                                       slr_stream_t stream);
+SLR_API slr_status slr_distill_backward(const void *logits, int64_t M, int64_t n_vocab, int64_t ldz, const int32_t *idx,
+                                        const float *teacher, int64_t k, float tau, const float *lse,
+                                        const float *dloss, void *dlogits, int64_t lddz, slr_stream_t stream);
+SLR_API slr_status slr_distill_loss_grad(const void *logits, int64_t M, int64_t n_vocab, int64_t ldz, const int32_t *idx,
+                                         const float *teacher, int64_t k, float tau, const float *dloss, float *loss,
+                                         void *dlogits, int64_t lddz, slr_stream_t stream);
+
 /* The two stages of slr_forward, for callers that schedule or time them
  * separately.  slr_forward(...) == slr_forward_project(...) followed on the same
  * stream by slr_forward_combine(...) with the same path and workspace.

@@ -20,6 +20,8 @@ Functions mirror the C ABI in ``include/slr.h``:
 * ``forward_epilogue(X, vals, meta, U, V, bias, act, residual) -> Y``  --
   ``slr_forward_epilogue``
 * ``epilogue_backward(dY, Z, act) -> (dZ, dbias)``  -- ``slr_epilogue_backward``
+* ``distill_forward(logits, idx, teacher) -> (loss, lse)``, ``distill_backward(...) -> dlogits``,
+  ``distill_loss_grad(...) -> (loss, dlogits)``  -- ``slr_distill_*``
 * ``workspace_size``, ``select_path``, ``check_kernel_error``
 
 Tensors are torch CUDA tensors (torch only provides memory and the current
@@ -96,6 +98,13 @@ def _load() -> ctypes.CDLL:
                                          ctypes.c_uint32, p]
     lib.slr_epilogue_backward.restype = st
     lib.slr_epilogue_backward.argtypes = [p, p, i64, i64, st, p, p, p]
+    f32 = ctypes.c_float
+    lib.slr_distill_forward.restype = st
+    lib.slr_distill_forward.argtypes = [p, i64, i64, i64, p, p, i64, f32, p, p, p]
+    lib.slr_distill_backward.restype = st
+    lib.slr_distill_backward.argtypes = [p, i64, i64, i64, p, p, i64, f32, p, p, p, i64, p]
+    lib.slr_distill_loss_grad.restype = st
+    lib.slr_distill_loss_grad.argtypes = [p, i64, i64, i64, p, p, i64, f32, p, p, p, i64, p]
     lib.slr_forward_workspace_size.restype = sz
     lib.slr_forward_workspace_size.argtypes = [i64, i64, i64, i64]
     lib.slr_forward_select_path.restype = st
@@ -451,6 +460,73 @@ def epilogue_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str, *, wan
     _check(_lib.slr_epilogue_backward(dY.data_ptr(), _addr(Z) if act != "none" else None, shape[0], shape[1], ACTS[act],
                                       _addr(out), _addr(dbias), stream), "slr_epilogue_backward")
     return (dY if out is None else out), dbias
+
+
+def _expect_logits(name: str, t: torch.Tensor, shape: tuple, device: torch.device) -> int:
+    """Leading dimension of bf16 logits, whose rows may be a slice of wider (padded) ones."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on {device} with unit column stride")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _distill_operands(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor):
+    if logits.dim() != 2 or idx.dim() != 2:
+        raise ValueError("logits and idx must be 2-D")
+    device, stream = _current(logits)
+    (M, n), k = logits.shape, idx.shape[1]
+    ldz = _expect_logits("logits", logits, (M, n), device)
+    _expect("idx", idx, torch.int32, (M, k), device)
+    _expect("teacher", teacher, torch.float32, (M, k), device)
+    return device, stream, M, n, k, ldz
+
+
+def distill_forward(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, *,
+                    tau: float = 1.0) -> tuple[torch.Tensor, torch.Tensor]:
+    """``(loss, lse)`` per token (fp32 [M]) of bf16 student ``logits`` [M, n_vocab]
+    against a teacher's top logits: columns ``idx`` (int32 [M, k], -1 where there
+    is none) and values ``teacher`` (fp32 [M, k]) at temperature ``tau``
+    (``slr_distill_forward``): tau^2 KL(p || softmax(logits / tau)), p the softmax
+    of the listed teacher logits."""
+    device, stream, M, n, k, ldz = _distill_operands(logits, idx, teacher)
+    loss = torch.empty(M, dtype=torch.float32, device=device)
+    lse = torch.empty(M, dtype=torch.float32, device=device)
+    _check(_lib.slr_distill_forward(logits.data_ptr(), M, n, ldz, idx.data_ptr(), teacher.data_ptr(), k, tau,
+                                    loss.data_ptr(), lse.data_ptr(), stream), "slr_distill_forward")
+    return loss, lse
+
+
+def distill_backward(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, lse: torch.Tensor,
+                     dloss: torch.Tensor, *, tau: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of :func:`distill_forward`'s losses with respect to the logits
+    (bf16) for the upstream ``dloss`` (fp32 [M]), from the forward's ``lse``
+    (``slr_distill_backward``).  ``out`` may be ``logits`` itself."""
+    device, stream, M, n, k, ldz = _distill_operands(logits, idx, teacher)
+    _expect("lse", lse, torch.float32, (M,), device)
+    _expect("dloss", dloss, torch.float32, (M,), device)
+    if out is None:
+        out = torch.empty((M, n), dtype=torch.bfloat16, device=device)
+    lddz = _expect_logits("out", out, (M, n), device)
+    _check(_lib.slr_distill_backward(logits.data_ptr(), M, n, ldz, idx.data_ptr(), teacher.data_ptr(), k, tau,
+                                     lse.data_ptr(), dloss.data_ptr(), out.data_ptr(), lddz, stream),
+           "slr_distill_backward")
+    return out
+
+
+def distill_loss_grad(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, dloss: torch.Tensor, *,
+                      tau: float = 1.0, out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """``(loss, dlogits)`` of :func:`distill_forward` and :func:`distill_backward`
+    in one pass over the logits, for weights ``dloss`` known beforehand
+    (``slr_distill_loss_grad``).  ``out`` may be ``logits`` itself."""
+    device, stream, M, n, k, ldz = _distill_operands(logits, idx, teacher)
+    _expect("dloss", dloss, torch.float32, (M,), device)
+    loss = torch.empty(M, dtype=torch.float32, device=device)
+    if out is None:
+        out = torch.empty((M, n), dtype=torch.bfloat16, device=device)
+    lddz = _expect_logits("out", out, (M, n), device)
+    _check(_lib.slr_distill_loss_grad(logits.data_ptr(), M, n, ldz, idx.data_ptr(), teacher.data_ptr(), k, tau,
+                                      dloss.data_ptr(), loss.data_ptr(), out.data_ptr(), lddz, stream),
+           "slr_distill_loss_grad")
+    return loss, out
 
 
 def forward_project(X: torch.Tensor, V: torch.Tensor | None, d_out: int, workspace: torch.Tensor, *,

@@ -23,6 +23,8 @@ bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0
 
 bool act_ok(int act) { return act >= SLR_ACT_NONE && act <= SLR_ACT_SILU; }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // sm_100 check, cached per device ordinal.
 slr_status check_device() {
     int dev = -1;
@@ -187,6 +189,24 @@ slr_status forward_impl(const void *X, int64_t M, const void *vals, const void *
     if (err == cudaSuccess)
         err = run_combine(X, M, vals, meta, d_out, d_in, U, r, Y, workspace, p, chained ? 2 : 1, stream, ep);
     return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
+}
+
+// Host checks shared by the distillation entry points; v1 and v2 are the call's
+// fp32 vectors (v1 required, v2 may be null), grad: it writes dlogits.
+slr_status distill_check(const void *logits, int64_t M, int64_t n, int64_t ldz, const int32_t *idx, const float *teacher,
+                         int64_t k, float tau, const void *v1, const void *v2, const void *dlogits, int64_t lddz,
+                         bool grad) {
+    if (!(tau >= 1e-4f && tau <= 1e4f)) return SLR_ERR_ARG;
+    if (M < 0 || n < 1 || k < 1 || k > SLR_DISTILL_MAX_K || M >= (int64_t(1) << 27) || n > INT32_MAX || ldz < n ||
+        (grad && (lddz < n || (dlogits == logits && lddz != ldz))))
+        return SLR_ERR_SHAPE;
+    if (M == 0) return SLR_OK;
+    if (logits == nullptr || idx == nullptr || teacher == nullptr || v1 == nullptr || (grad && dlogits == nullptr))
+        return SLR_ERR_NULL;
+    if (!aligned2(logits) || !aligned4(idx) || !aligned4(teacher) || !aligned4(v1) || !aligned4(v2) ||
+        (grad && !aligned2(dlogits)))
+        return SLR_ERR_ALIGN;
+    return check_device();
 }
 
 }  // namespace
@@ -519,6 +539,45 @@ slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t M, int64
         err = slr::launch_epilogue_backward(static_cast<const uint16_t *>(dY), static_cast<const uint16_t *>(Z), M, d_out,
                                             (int)act, static_cast<uint16_t *>(dZ), db, st);
     }
+    return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
+}
+
+slr_status slr_distill_forward(const void *logits, int64_t M, int64_t n_vocab, int64_t ldz, const int32_t *idx,
+                               const float *teacher, int64_t k, float tau, float *loss, float *lse,
+                               slr_stream_t stream) {
+    const slr_status s = slr::distill_check(logits, M, n_vocab, ldz, idx, teacher, k, tau, loss, lse, nullptr, 0, false);
+    if (s != SLR_OK || M == 0) return s;
+    const cudaError_t err =
+        slr::launch_distill_forward(static_cast<const uint16_t *>(logits), M, n_vocab, ldz, idx, teacher, k, tau, loss,
+                                    lse, reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
+}
+
+slr_status slr_distill_backward(const void *logits, int64_t M, int64_t n_vocab, int64_t ldz, const int32_t *idx,
+                                const float *teacher, int64_t k, float tau, const float *lse, const float *dloss,
+                                void *dlogits, int64_t lddz, slr_stream_t stream) {
+    if (M > 0 && dloss == nullptr) return SLR_ERR_NULL;
+    const slr_status s =
+        slr::distill_check(logits, M, n_vocab, ldz, idx, teacher, k, tau, lse, dloss, dlogits, lddz, true);
+    if (s != SLR_OK || M == 0) return s;
+    const cudaError_t err =
+        slr::launch_distill_backward(static_cast<const uint16_t *>(logits), M, n_vocab, ldz, idx, teacher, k, tau, lse,
+                                     dloss, static_cast<uint16_t *>(dlogits), lddz,
+                                     reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
+}
+
+slr_status slr_distill_loss_grad(const void *logits, int64_t M, int64_t n_vocab, int64_t ldz, const int32_t *idx,
+                                 const float *teacher, int64_t k, float tau, const float *dloss, float *loss,
+                                 void *dlogits, int64_t lddz, slr_stream_t stream) {
+    if (M > 0 && dloss == nullptr) return SLR_ERR_NULL;
+    const slr_status s =
+        slr::distill_check(logits, M, n_vocab, ldz, idx, teacher, k, tau, loss, dloss, dlogits, lddz, true);
+    if (s != SLR_OK || M == 0) return s;
+    const cudaError_t err =
+        slr::launch_distill_loss_grad(static_cast<const uint16_t *>(logits), M, n_vocab, ldz, idx, teacher, k, tau,
+                                      dloss, loss, static_cast<uint16_t *>(dlogits), lddz,
+                                      reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
 }
 

@@ -155,4 +155,16 @@ cudaError_t launch_decode_forward(const uint16_t *X, int64_t M, const uint16_t *
 cudaError_t launch_epilogue_backward(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t d_out, int act,
                                      uint16_t *dZ, float *db, cudaStream_t stream);
 
+// Distillation from a teacher's top logits (distill.cu): the loss and lse, the
+// gradient from a given lse, or loss and gradient in one pass.  1 <= M < 2^27,
+// 1 <= n < 2^31, 1 <= k <= SLR_DISTILL_MAX_K.
+cudaError_t launch_distill_forward(const uint16_t *z, int64_t M, int64_t n, int64_t ldz, const int32_t *idx,
+                                   const float *t, int64_t k, float tau, float *loss, float *lse, cudaStream_t stream);
+cudaError_t launch_distill_backward(const uint16_t *z, int64_t M, int64_t n, int64_t ldz, const int32_t *idx,
+                                    const float *t, int64_t k, float tau, const float *lse, const float *dloss,
+                                    uint16_t *dz, int64_t lddz, cudaStream_t stream);
+cudaError_t launch_distill_loss_grad(const uint16_t *z, int64_t M, int64_t n, int64_t ldz, const int32_t *idx,
+                                     const float *t, int64_t k, float tau, const float *dloss, float *loss,
+                                     uint16_t *dz, int64_t lddz, cudaStream_t stream);
+
 }  // namespace slr
