@@ -29,8 +29,9 @@ def distill(z: np.ndarray, idx: np.ndarray, t: np.ndarray, tau: float):
         logp = x - (x.max() + np.log(np.exp(x - x.max()).sum()))
         p = np.exp(logp)
         y = z[m] / tau
-        lse[m] = y.max() + np.log(np.exp(y - y.max()).sum())
-        logq = y - lse[m]
+        logs = np.log(np.exp(y - y.max()).sum())
+        lse[m] = y.max() + logs
+        logq = (y - y.max()) - logs   # not y - lse: next to the type's lowest values lse has no digits left for logs
         term = np.where(p > 0, p * (logp - logq[cols]), 0.0)
         loss[m] = tau ** 2 * term.sum()
         spread[m] = np.abs(term).sum()

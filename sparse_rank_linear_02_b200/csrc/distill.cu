@@ -22,7 +22,18 @@
 //
 // Rows start at any 2-byte boundary: a row is cut into a head up to the first
 // 16-byte boundary, vectors, and a tail.
+//
+// Measured, k = 64, against the copy bandwidth: 4096 x 131072 forward 163 us
+// (1.01), backward 339 (0.97), both in one pass 496 (0.66); 4096 x 32000 49 / 97
+// / 133 us; one token of 131072 6.3 / 6.6 / 8.3 us.  The one pass is short of
+// its 4 bytes a logit because most of its second reads miss L2 again (two thirds
+// by the counters, with a row per SM in flight).  Tried and not kept for it: a
+// persistent CTA per SM that keeps a row in shared memory (502 us: its two
+// passes take turns with HBM), the gradient of one row beside the statistics of
+// the next (525 us read from L2, 666 us kept in clusters of two), and clusters
+// that keep the row in registers (610 to 644 us: two cluster barriers a row).
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "tc_ptx.cuh"
 
 namespace slr {
@@ -30,7 +41,7 @@ namespace {
 
 constexpr int kMaxK = SLR_DISTILL_MAX_K;
 constexpr int kNV = 8;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Coherent loads: the gradient may overwrite the logits.
 __device__ __forceinline__ uint4 ld_v4(const uint16_t *p) {
@@ -55,52 +66,39 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// A running maximum and the sum of 2^(z c + b), c = log2(e) / tau, b = -max c as
-// rounded: every later use adds the same b, so its rounding drops out of the
-// logarithms.  With no finite maximum yet b is 0, so that 2^-inf = 0 and no
-// difference of infinities arises; an empty sum stays 0 whatever its factor.
+// A running maximum and the sum of 2^((z - max) c), c = log2(e) / tau.  The
+// difference comes first: it is exact or rounded once, and a logit of the type's
+// lowest value (a mask) overflows nothing.  With no finite maximum yet the
+// reference is 0, so that 2^-inf = 0 and no difference of infinities arises; an
+// empty sum stays 0 whatever its factor.
 struct MaxSum {
-    float m, b, s;
+    float m, s;
+    __device__ __forceinline__ float ref() const { return m == -INFINITY ? 0.f : m; }
     __device__ __forceinline__ void raise(float to, float c) {
-        const float old = b;
+        const float old = ref();
         m = fmaxf(m, to);
-        b = m == -INFINITY ? 0.f : -m * c;
-        s = s == 0.f ? 0.f : s * ex2(b - old);
+        s = s == 0.f ? 0.f : s * ex2((old - ref()) * c);
     }
     __device__ __forceinline__ void add(float z, float c) {
         raise(z, c);
-        s += ex2(fmaf(z, c, b));
-    }
-    __device__ __forceinline__ void join(float om, float os, float c) {
-        const float ob = om == -INFINITY ? 0.f : -om * c;
-        raise(om, c);
-        s += os == 0.f ? 0.f : os * ex2(b - ob);
+        s += ex2((z - ref()) * c);
     }
 };
 
-template <int T>
-__device__ __forceinline__ float block_sum(float v, float *red) {
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < T / 32; ++w) v += red[w];
     return v;
 }
-template <int T>
-__device__ __forceinline__ float block_max(float v, float *red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < T / 32; ++w) v = fmaxf(v, red[w]);
-    return v;
+// The lanes' pairs joined: the maximum first, then each sum rescaled once.
+__device__ __forceinline__ void warp_join(MaxSum &r, float c) {
+    r.raise(warp_max(r.m), c);
+    r.s = warp_sum(r.s);
 }
 
 __device__ __forceinline__ void st_cluster_f32(const float *local, uint32_t rank, float v) {
@@ -123,16 +121,17 @@ struct DistillArgs {
 
 template <int T, bool kLoss, bool kGrad>
 __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_constant__ DistillArgs a) {
-    __shared__ int32_t sh_i[kMaxK];
+    constexpr int kWarps = T / 32;
+    __shared__ __align__(16) int32_t sh_i[kMaxK];
     __shared__ float sh_p[kMaxK], sh_z[kMaxK];
-    __shared__ float red[T / 32], red2[T / 32];
+    __shared__ float row_m[kWarps], row_s[kWarps], tea_m[kWarps], tea_s[kWarps], part_w[kWarps];
     __shared__ float peer_m[8], peer_s[8], peer_l[8];
     uint32_t ks_n;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ks_n));
     const uint32_t ks_q = tc::cluster_ctarank();
     const int64_t m = blockIdx.x / ks_n;
-    const int tid = threadIdx.x, k = a.k;
-    const float c = kLog2e / a.tau, itau = 1.0f / a.tau;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
+    const float c = kLog2e / a.tau;
 
     // This CTA's slice [lo, hi): vectors [v0, v1) of the row, with the head on
     // the first CTA and the tail on the last.
@@ -143,29 +142,80 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
     const int64_t v0 = nv * ks_q / ks_n, v1 = nv * (ks_q + 1) / ks_n;
     const int64_t lo = ks_q == 0 ? 0 : head + 8 * v0, hi = ks_q == ks_n - 1 ? a.n : head + 8 * v1;
     const int64_t tail = head + 8 * nv;   // first column of the row's tail
-    const uint16_t *zv = z + head;
+    const bool has_head = ks_q == 0 && tid < head;
+    const bool has_tail = ks_q == ks_n - 1 && tid < a.n - tail;
 
-    // Teacher entries: probabilities and the slice's listed logits.
-    float tmax = -INFINITY;
+    // The first vectors are requested before anything is waited for: the
+    // teacher's entries and their statistics are worked on while they come.
+    uint4 x[kNV];
+    const bool fits = v1 - v0 <= (int64_t)T * kNV;
+    auto load = [&](int64_t b) {
+#pragma unroll
+        for (int u = 0; u < kNV; ++u) {
+            const int64_t v = b + tid + (int64_t)u * T;
+            x[u] = v < v1 ? ld_v4(z + head + 8 * v) : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
+        }
+    };
+    load(v0);
+    const float zhead = has_head ? ld_z(z + tid) : 0.f, ztail = has_tail ? ld_z(z + tail + tid) : 0.f;
+    const float w = kGrad ? __ldg(a.dloss + m) * a.tau : 0.f;
+
+    // Teacher entries, their maximum and sum, and the slice's listed logits.  A
+    // NaN logit is kept as the maximum's mark (+inf would give NaN as well).
+    MaxSum t{-INFINITY, 0.f};
+    if (tid < 3 && k + tid < kMaxK) sh_i[k + tid] = -1;   // read with the list, four at a time
     for (int j = tid; j < k; j += T) {
         const int32_t i = __ldg(a.idx + m * k + j);
         const bool there = i >= 0 && i < a.n;
-        const float t = there ? __ldg(a.t + m * k + j) : -INFINITY;
-        sh_i[j] = t == -INFINITY ? -1 : i;
-        sh_p[j] = t;
+        const float v = there ? __ldg(a.t + m * k + j) : -INFINITY;
+        sh_i[j] = v == -INFINITY ? -1 : i;
+        sh_p[j] = v;
         sh_z[j] = there && i >= lo && i < hi ? ld_z(z + i) : 0.f;
-        tmax = t != t ? t : (tmax != tmax ? tmax : fmaxf(tmax, t));
+        t.add(v != v ? INFINITY : v, c);
     }
-    // NaN teacher logits give a NaN loss; fmaxf alone would drop them.
-    const bool tnan = __syncthreads_or(tmax != tmax);
-    tmax = block_max<T>(tmax != tmax ? -INFINITY : tmax, red);
-    const bool empty = tmax == -INFINITY && !tnan;
-    const float w = kGrad ? __ldg(a.dloss + m) * a.tau : 0.f;
+    warp_join(t, c);
+    if (lane == 0) {
+        tea_m[warp] = t.m;
+        tea_s[warp] = t.s;
+    }
 
-    if (empty && kLoss && ks_q == 0 && tid == 0) {
-        a.loss[m] = 0.f;
-        if (a.lse != nullptr) a.lse[m] = 0.f;
+    // Statistics of the row's slice; kept in registers where it fits.
+    MaxSum r{-INFINITY, 0.f};
+    if constexpr (kLoss) {
+        if (has_head) r.add(zhead, c);
+        if (has_tail) r.add(ztail, c);
+        for (int64_t b = v0; b < v1; b += (int64_t)T * kNV) {
+            if (b != v0) load(b);
+            uint32_t mx = 0xFF80FF80u;
+#pragma unroll
+            for (int u = 0; u < kNV; ++u)
+                mx = max_bf16x2(mx, max_bf16x2(max_bf16x2(x[u].x, x[u].y), max_bf16x2(x[u].z, x[u].w)));
+            r.raise(fmaxf(bf16lo_to_f32(mx), bf16hi_to_f32(mx)), c);
+            const f32x2 neg = dup2(-r.ref()), c2 = dup2(c);
+            f32x2 sum = dup2(0.f);
+#pragma unroll
+            for (int u = 0; u < kNV; ++u) {
+                const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum = add2(sum, exp2_2(mul2(add2(pack2(bf16lo_to_f32(xw[i]), bf16hi_to_f32(xw[i])), neg), c2)));
+            }
+            float s0, s1;
+            unpack2(sum, s0, s1);
+            r.s += s0 + s1;
+        }
+        warp_join(r, c);
+        if (lane == 0) {
+            row_m[warp] = r.m;
+            row_s[warp] = r.s;
+        }
     }
+    __syncthreads();
+    t = MaxSum{lane < kWarps ? tea_m[lane] : -INFINITY, lane < kWarps ? tea_s[lane] : 0.f};
+    warp_join(t, c);
+    const bool empty = t.m == -INFINITY;
+    const float t_ref = t.ref(), t_log = log2f(t.s);   // log2 p_j = (t_j - t_ref) c - t_log
+
     uint16_t *dz = kGrad ? a.dz + m * a.lddz : nullptr;
     const bool same_phase = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     auto put8 = [&](int64_t v, const uint32_t (&o)[4]) {
@@ -177,122 +227,74 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
             for (int i = 0; i < 8; ++i) at[i] = (uint16_t)(o[i / 2] >> (16 * (i & 1)));
         }
     };
-    if (empty || (!kLoss && w == 0.f)) {   // uniform over the cluster: nothing of the row is read
-        if constexpr (kGrad) {
-            const uint32_t zero[4] = {0, 0, 0, 0};
-            for (int64_t v = v0 + tid; v < v1; v += T) put8(v, zero);
-            if (ks_q == 0 && tid < head) dz[tid] = 0;
-            if (ks_q == ks_n - 1 && tid < a.n - tail) dz[tail + tid] = 0;
-        }
-        return;
-    }
-    float logsum_t = 0.f;
-    {
-        float e = 0.f;
-        for (int j = tid; j < k; j += T) {
-            const float x = sh_i[j] < 0 ? 0.f : expf((sh_p[j] - tmax) * itau);
-            e += x;
-        }
-        e = block_sum<T>(e, red);
-        logsum_t = logf(e);
-    }
-
-    // Statistics of the row, the slice kept in registers where it fits.
-    uint4 x[kNV];
-    const bool fits = v1 - v0 <= (int64_t)T * kNV;
-    float edge = 0.f;        // this thread's head or tail logit
-    const bool has_edge = ks_q == 0 && tid < head;
-    const bool has_tail = ks_q == ks_n - 1 && tid < a.n - tail;
-    float edge2 = 0.f;
-    if (has_edge) edge = ld_z(z + tid);
-    if (has_tail) edge2 = ld_z(z + tail + tid);
-    auto load = [&](int64_t b) {
-#pragma unroll
-        for (int u = 0; u < kNV; ++u) {
-            const int64_t v = b + tid + (int64_t)u * T;
-            x[u] = v < v1 ? ld_v4(zv + 8 * v) : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
-        }
-    };
-    float shift;   // q = exp2(z c - shift)
+    // log2 q = (z scale - ref) c - logs: with the forward's statistics scale is 1
+    // and ref the row's maximum; from a given lse scale is 1 / tau, ref that lse,
+    // the factor log2(e) and logs 0.
+    float scale = 1.f, ref = 0.f, fac = c, logs = 0.f;
     if constexpr (kLoss) {
-        MaxSum r{-INFINITY, 0.f, 0.f};
-        if (has_edge) r.add(edge, c);
-        if (has_tail) r.add(edge2, c);
-        for (int64_t b = v0; b < v1; b += (int64_t)T * kNV) {
-            load(b);
-            uint32_t mx = 0xFF80FF80u;
-#pragma unroll
-            for (int u = 0; u < kNV; ++u)
-                mx = max_bf16x2(mx, max_bf16x2(max_bf16x2(x[u].x, x[u].y), max_bf16x2(x[u].z, x[u].w)));
-            r.raise(fmaxf(bf16lo_to_f32(mx), bf16hi_to_f32(mx)), c);
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int u = 0; u < kNV; ++u) {
-                const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s0 += ex2(fmaf(bf16lo_to_f32(xw[i]), c, r.b));
-                    s1 += ex2(fmaf(bf16hi_to_f32(xw[i]), c, r.b));
-                }
-            }
-            r.s += s0 + s1;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            r.join(__shfl_xor_sync(0xFFFFFFFFu, r.m, o), __shfl_xor_sync(0xFFFFFFFFu, r.s, o), c);
-        __syncthreads();
-        if ((tid & 31) == 0) {
-            red[tid >> 5] = r.m;
-            red2[tid >> 5] = r.s;
-        }
-        __syncthreads();
-        r = MaxSum{-INFINITY, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < T / 32; ++i) r.join(red[i], red2[i], c);
+        r = MaxSum{lane < kWarps ? row_m[lane] : -INFINITY, lane < kWarps ? row_s[lane] : 0.f};
+        warp_join(r, c);
         if (ks_n > 1) {
             if (tid < (int)ks_n) {
                 st_cluster_f32(&peer_m[ks_q], tid, r.m);
                 st_cluster_f32(&peer_s[ks_q], tid, r.s);
             }
             tc::cluster_sync_all();
-            r = MaxSum{-INFINITY, 0.f, 0.f};
-            for (uint32_t q = 0; q < ks_n; ++q) r.join(peer_m[q], peer_s[q], c);
+            r = MaxSum{lane < (int)ks_n ? peer_m[lane] : -INFINITY, lane < (int)ks_n ? peer_s[lane] : 0.f};
+            warp_join(r, c);
         }
-        const float logs = log2f(r.s);
+        ref = r.ref();
+        logs = log2f(r.s);
+    } else {
+        scale = 1.f / a.tau;
+        ref = __ldg(a.lse_in + m);
+        fac = kLog2e;
+    }
+    // The entries' probabilities, and their terms of the loss.
+    if (32 * warp < k) {
         float part = 0.f;
         for (int j = tid; j < k; j += T) {
             const int32_t i = sh_i[j];
-            if (i < 0) continue;
-            const float logp = (sh_p[j] - tmax) * itau - logsum_t, p = expf(logp);
-            if (i >= lo && i < hi && !(p == 0.f)) part += p * (logp - kLn2 * (fmaf(sh_z[j], c, r.b) - logs));
+            const float logp = fmaf(sh_p[j] - t_ref, c, -t_log), p = i < 0 ? 0.f : exp2f(logp);
+            sh_p[j] = p;
+            if (kLoss && i >= lo && i < hi && !(p == 0.f)) part += p * (logp - fmaf(sh_z[j] - ref, c, -logs));
         }
-        part = block_sum<T>(part, red);
-        if (ks_n > 1) {
-            if (tid == 0) st_cluster_f32(&peer_l[ks_q], 0, part);
-            tc::cluster_sync_all();   // the parts are in the first CTA's shared memory, which reads its own
-            if (ks_q == 0) {
-                part = peer_l[0];
-                for (uint32_t q = 1; q < ks_n; ++q) part += peer_l[q];
+        if constexpr (kLoss) {
+            part = warp_sum(part);
+            if (lane == 0) part_w[warp] = part;
+        }
+    }
+    if constexpr (kLoss) {
+        __syncthreads();
+        float part = 0.f;
+        if (warp == 0) {
+            part = warp_sum(lane < kWarps && 32 * lane < k ? part_w[lane] : 0.f);
+            if (ks_n > 1 && lane == 0) st_cluster_f32(&peer_l[ks_q], 0, part);
+        }
+        if (ks_n > 1) tc::cluster_sync_all();   // the parts are in the first CTA's shared memory, which alone reads them
+        if (ks_q == 0 && warp == 0) {
+            if (ks_n > 1) part = warp_sum(lane < (int)ks_n ? peer_l[lane] : 0.f);
+            if (lane == 0) {
+                a.loss[m] = empty ? 0.f : a.tau * a.tau * kLn2 * part;
+                if (a.lse != nullptr) a.lse[m] = empty ? 0.f : fmaf(kLn2, logs, ref / a.tau);
             }
         }
-        if (ks_q == 0 && tid == 0) {
-            a.loss[m] = a.tau * a.tau * (tnan ? NAN : part);
-            if (a.lse != nullptr) a.lse[m] = kLn2 * (logs - r.b);
-        }
-        shift = logs - r.b;
-    } else {
-        shift = __ldg(a.lse_in + m) * kLog2e;
     }
     if constexpr (kGrad) {
-        if (kLoss && w == 0.f) {   // a token without weight: its row is zero whatever its logits
+        if (empty || w == 0.f) {   // a token without entries or weight: zero whatever its logits
             const uint32_t zero[4] = {0, 0, 0, 0};
             for (int64_t v = v0 + tid; v < v1; v += T) put8(v, zero);
-            if (has_edge) dz[tid] = 0;
+            if (has_head) dz[tid] = 0;
             if (has_tail) dz[tail + tid] = 0;
             return;
         }
+        const f32x2 scale2 = dup2(scale), nref2 = dup2(-ref), fac2 = dup2(fac), nlogs2 = dup2(-logs);
+        auto q2 = [&](f32x2 zz) {
+            return exp2_2(kLoss ? fma2(add2(zz, nref2), fac2, nlogs2) : mul2(fma2(zz, scale2, nref2), fac2));
+        };
+        auto q1 = [&](float zz) { return ex2(kLoss ? fmaf(zz - ref, fac, -logs) : fmaf(zz, scale, -ref) * fac); };
         for (int64_t b = v0; b < v1; b += (int64_t)T * kNV) {
-            if (!kLoss || !fits) load(b);
+            if (b != v0 || (kLoss && !fits)) load(b);
 #pragma unroll
             for (int u = 0; u < kNV; ++u) {
                 const int64_t v = b + tid + (int64_t)u * T;
@@ -301,24 +303,30 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
                     uint32_t o[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float g0 = w * ex2(fmaf(bf16lo_to_f32(xw[i]), c, -shift));
-                        const float g1 = w * ex2(fmaf(bf16hi_to_f32(xw[i]), c, -shift));
+                        float g0, g1;
+                        unpack2(mul2(dup2(w), q2(pack2(bf16lo_to_f32(xw[i]), bf16hi_to_f32(xw[i])))), g0, g1);
                         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(g1), "f"(g0));
                     }
                     put8(v, o);
                 }
             }
         }
-        if (has_edge) dz[tid] = f32_to_bf16_bits(w * ex2(fmaf(edge, c, -shift)));
-        if (has_tail) dz[tail + tid] = f32_to_bf16_bits(w * ex2(fmaf(edge2, c, -shift)));
+        if (has_head) dz[tid] = f32_to_bf16_bits(w * q1(zhead));
+        if (has_tail) dz[tail + tid] = f32_to_bf16_bits(w * q1(ztail));
         __syncthreads();   // the listed columns below overwrite what other threads wrote
         for (int j = tid; j < k; j += T) {
             const int32_t i = sh_i[j];
             if (i < lo || i >= hi) continue;
             float p = 0.f;
-            for (int l = 0; l < k; ++l)
-                if (sh_i[l] == i) p += expf((sh_p[l] - tmax) * itau - logsum_t);
-            dz[i] = f32_to_bf16_bits(w * (ex2(fmaf(sh_z[j], c, -shift)) - (tnan ? NAN : p)));
+#pragma unroll 4
+            for (int l = 0; l < k; l += 4) {
+                const int4 at = *reinterpret_cast<const int4 *>(sh_i + l);
+                if (at.x == i) p += sh_p[l];
+                if (at.y == i) p += sh_p[l + 1];
+                if (at.z == i) p += sh_p[l + 2];
+                if (at.w == i) p += sh_p[l + 3];
+            }
+            dz[i] = f32_to_bf16_bits(w * (q1(sh_z[j]) - p));
         }
     }
 }
@@ -345,9 +353,18 @@ cudaError_t launch_distill(const DistillArgs &a, cudaStream_t stream) {
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t vecs = a.n / 8;   // of eight logits, at most
     if (vecs <= 128 * kNV) return launch_t<128, kLoss, kGrad>(a, 1, stream);
+    // Few rows: as many threads on each as a cluster gives (64 x 131072: 9.5 /
+    // 12.2 / 15.0 us forward / backward / both with 8 x 256, 21.4 / 32.1 / 47.7
+    // with 1 x 128).  Many: small CTAs, eight to an SM, hide each other's
+    // reductions (4096 x 131072 forward: 163 us with 1 x 128, 178 with 1 x 512,
+    // 361 with 4 x 512); a gradient's pass wants slices of at most 32768 logits
+    // (338 us with 4 x 128, 375 with 1 x 128; 1000 x 50001: 40.8 with 2 x 128,
+    // 43.2 with 1 x 128).
+    if (a.M * 8 < 5 * (int64_t)sms && vecs > 8 * 256) return launch_t<256, kLoss, kGrad>(a, 8, stream);
     unsigned ks = 1;
-    while (ks < 8 && (vecs > (int64_t)ks * 512 * kNV || a.M * ks < 2 * (int64_t)sms) && vecs > (int64_t)ks * 512) ks *= 2;
-    return launch_t<512, kLoss, kGrad>(a, ks, stream);
+    while (ks < 8 && ((kGrad && a.n > (int64_t)ks * 32768) || (a.M * ks < 5 * (int64_t)sms && vecs > (int64_t)ks * 256)))
+        ks *= 2;
+    return launch_t<128, kLoss, kGrad>(a, ks, stream);
 }
 
 }  // namespace

@@ -21,6 +21,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace slr {
 
@@ -35,51 +36,6 @@ struct Epilogue {
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
-
-// Two fp32 values in one register pair: the arithmetic below runs on
-// fma.rn.f32x2 and its kin, one issue slot for two results.  Written one value
-// at a time, the slopes bound the backward kernel by instruction issue.
-typedef uint64_t f32x2;
-__device__ __forceinline__ f32x2 pack2(float a, float b) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 dup2(float a) { return pack2(a, a); }
-__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-// 2^a and 1/a of both values: one special-function operation each.
-__device__ __forceinline__ f32x2 exp2_2(f32x2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
-    return pack2(a, b);
-}
-__device__ __forceinline__ f32x2 rcp2(f32x2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
-    return pack2(a, b);
-}
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Phi(z), given e = exp(-z^2 / 2).
 __device__ __forceinline__ f32x2 normal_cdf2(f32x2 z, f32x2 e) {
