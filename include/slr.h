@@ -461,6 +461,41 @@ SLR_API slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t 
                                          void *dZ, float *db, slr_stream_t stream);
 
 /* --------------------------------------------------------------------------
+ * Backward with respect to the layer's input.
+ *
+ *        dX = dY * S + (dY * U) * V
+ *
+ * for an upstream gradient dY of X S^T + (X V^T) U^T (LoSparse section 3.2): what
+ * carries the gradient to the layer before, beside slr_lora_backward's dU and dV
+ * (S stays fixed).  S is 2:4 along the output dimension of this product, so the
+ * kernel expands it to a dense tensor-core operand on the way into shared
+ * memory.
+ *
+ *   dY    device, bf16 [M, d_out].
+ *   vals, meta, U, V  the layer as slr_forward takes it (U, V may be NULL when
+ *         r == 0).
+ *   dX    device, bf16 [M, d_in], out.
+ *   workspace  slr_input_backward_workspace_size() bytes, 256-byte aligned (G =
+ *         dY U, and partial tiles where a short batch splits the sum; the size
+ *         is computed for the current device).
+ *
+ * fp32 accumulation; G is rounded to bf16 between the products (the tensor cores
+ * read bf16), dX once.  Deterministic: where the sum over d_out is split, the
+ * fp32 partials are added in slice order.  Accuracy (tested): as slr_forward's
+ * contract, with B = |dY| |S| + |dY| |U| |V|.
+ *
+ * Requirements: M >= 0 (M == 0 does nothing), d_out >= 8 with d_out % 8 == 0,
+ * d_in >= 128 with d_in % 128 == 0, 0 <= r <= 256 with r % 8 == 0, M, d_out, d_in
+ * < 2^31; all pointers 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+SLR_API slr_status slr_input_backward(const void *dY, int64_t M, const void *vals, const void *meta, int64_t d_out,
+                                      int64_t d_in, const void *U, const void *V, int64_t r, void *dX, void *workspace,
+                                      size_t workspace_bytes, slr_stream_t stream);
+
+/* Scratch bytes of slr_input_backward for this problem on the current device. */
+SLR_API size_t slr_input_backward_workspace_size(int64_t M, int64_t d_out, int64_t d_in, int64_t r);
+
+/* --------------------------------------------------------------------------
  * Distillation of a student's logits from a teacher's top logits.
  *
  * The recovery of a compressed model trains against the dense one (LoSparse

@@ -20,6 +20,7 @@ Functions mirror the C ABI in ``include/slr.h``:
 * ``forward_epilogue(X, vals, meta, U, V, bias, act, residual) -> Y``  --
   ``slr_forward_epilogue``
 * ``epilogue_backward(dY, Z, act) -> (dZ, dbias)``  -- ``slr_epilogue_backward``
+* ``input_backward(dY, vals, meta, U, V) -> dX``  -- ``slr_input_backward``
 * ``distill_forward(logits, idx, teacher) -> (loss, lse)``, ``distill_backward(...) -> dlogits``,
   ``distill_loss_grad(...) -> (loss, dlogits)``  -- ``slr_distill_*``
 * ``workspace_size``, ``select_path``, ``check_kernel_error``
@@ -98,6 +99,10 @@ def _load() -> ctypes.CDLL:
                                          ctypes.c_uint32, p]
     lib.slr_epilogue_backward.restype = st
     lib.slr_epilogue_backward.argtypes = [p, p, i64, i64, st, p, p, p]
+    lib.slr_input_backward.restype = st
+    lib.slr_input_backward.argtypes = [p, i64, p, p, i64, i64, p, p, i64, p, p, sz, p]
+    lib.slr_input_backward_workspace_size.restype = sz
+    lib.slr_input_backward_workspace_size.argtypes = [i64, i64, i64, i64]
     f32 = ctypes.c_float
     lib.slr_distill_forward.restype = st
     lib.slr_distill_forward.argtypes = [p, i64, i64, i64, p, p, i64, f32, p, p, p]
@@ -460,6 +465,32 @@ def epilogue_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str, *, wan
     _check(_lib.slr_epilogue_backward(dY.data_ptr(), _addr(Z) if act != "none" else None, shape[0], shape[1], ACTS[act],
                                       _addr(out), _addr(dbias), stream), "slr_epilogue_backward")
     return (dY if out is None else out), dbias
+
+
+def input_backward_workspace_size(M: int, d_out: int, d_in: int, r: int) -> int:
+    return int(_lib.slr_input_backward_workspace_size(M, d_out, d_in, r))
+
+
+def input_backward(dY: torch.Tensor, vals: torch.Tensor, meta: torch.Tensor, U: torch.Tensor | None,
+                   V: torch.Tensor | None, *, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of the layer's input for upstream ``dY`` [M, d_out]:
+    ``dX = dY @ S + (dY @ U) @ V`` (bf16 [M, d_in]; ``slr_input_backward``)."""
+    if dY.dim() != 2:
+        raise ValueError("dY must be 2-D")
+    device, stream = _current(dY)
+    M = dY.shape[0]
+    d_out, d_in, r = _expect_layer(vals, meta, U, V, device)
+    _expect("dY", dY, torch.bfloat16, (M, d_out), device)
+    if out is None:
+        out = torch.empty((M, d_in), dtype=torch.bfloat16, device=device)
+    else:
+        _expect("out", out, torch.bfloat16, (M, d_in), device)
+    workspace, ws_bytes = _scratch(
+        workspace, 0 if workspace is not None else input_backward_workspace_size(M, d_out, d_in, r), device)
+    _check(_lib.slr_input_backward(dY.data_ptr(), M, vals.data_ptr(), meta.data_ptr(), d_out, d_in, _addr(U), _addr(V), r,
+                                   out.data_ptr(), _addr(workspace), ws_bytes, stream), "slr_input_backward")
+    return out
 
 
 def _expect_logits(name: str, t: torch.Tensor, shape: tuple, device: torch.device) -> int:

@@ -56,6 +56,17 @@ slr_status check_device() {
 constexpr int64_t kDecodeMaxM = 1;
 constexpr int64_t kDecodeMaxWeights = int64_t(1) << 26;
 
+// SMs of the current device; without one, a B200's.
+int current_sms() {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        sms = 148;
+    }
+    return sms;
+}
+
 size_t workspace_bytes_for(int64_t M, int64_t r, slr_path path) {
     if (M <= 0 || r <= 0) return 0;
     if (path == SLR_PATH_DECODE) return round_up((size_t)M * r * sizeof(float), kAlign);
@@ -63,13 +74,7 @@ size_t workspace_bytes_for(int64_t M, int64_t r, slr_path path) {
     // kernel with its projection phase and K-split last round: T, counters,
     // partial products and partial tiles.
     if (M > kChainMaxM) {
-        int dev = 0, sms = 148;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-            cudaGetLastError();
-            sms = 148;   // no device: size for a B200
-        }
-        return round_up(fused_layout(M, r, fused_pairs_for(sms)).bytes, kAlign);
+        return round_up(fused_layout(M, r, fused_pairs_for(current_sms())).bytes, kAlign);
     }
     return round_up((size_t)M * r * sizeof(uint16_t), kAlign);
 }
@@ -432,12 +437,13 @@ slr_path slr_forward_select_path(int64_t M, int64_t d_out, int64_t d_in, int64_t
 slr_status slr_check_kernel_error(void) {
     if (slr::check_device() != SLR_OK) return SLR_ERR_DEVICE;
     if (cudaDeviceSynchronize() != cudaSuccess) return SLR_ERR_CUDA;
-    unsigned code = 0, code28 = 0, code_bwd = 0, code_am = 0;
+    unsigned code = 0, code28 = 0, code_bwd = 0, code_am = 0, code_dx = 0;
     if (slr::read_and_clear_kernel_error(&code) != cudaSuccess) return SLR_ERR_CUDA;
     if (slr::read_and_clear_decode28_error(&code28) != cudaSuccess) return SLR_ERR_CUDA;
     if (slr::read_and_clear_backward_error(&code_bwd) != cudaSuccess) return SLR_ERR_CUDA;
     if (slr::read_and_clear_am_error(&code_am) != cudaSuccess) return SLR_ERR_CUDA;
-    return (code | code28 | code_bwd | code_am) ? SLR_ERR_TIMEOUT : SLR_OK;
+    if (slr::read_and_clear_dx_error(&code_dx) != cudaSuccess) return SLR_ERR_CUDA;
+    return (code | code28 | code_bwd | code_am | code_dx) ? SLR_ERR_TIMEOUT : SLR_OK;
 }
 
 int64_t slr_plan_check(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int32_t kernel, int32_t tail_mode,
@@ -578,6 +584,38 @@ slr_status slr_distill_loss_grad(const void *logits, int64_t M, int64_t n_vocab,
         slr::launch_distill_loss_grad(static_cast<const uint16_t *>(logits), M, n_vocab, ldz, idx, teacher, k, tau,
                                       dloss, loss, static_cast<uint16_t *>(dlogits), lddz,
                                       reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
+}
+
+size_t slr_input_backward_workspace_size(int64_t M, int64_t d_out, int64_t d_in, int64_t r) {
+    if (M <= 0 || d_out < 8 || d_in < 128 || d_in % 128 != 0 || r < 0 || r > 256 || M > INT32_MAX || d_out > INT32_MAX ||
+        d_in > INT32_MAX)
+        return 0;
+    return slr::round_up(slr::input_backward_workspace(M, d_out, d_in, r, slr::current_sms()), slr::kAlign);
+}
+
+slr_status slr_input_backward(const void *dY, int64_t M, const void *vals, const void *meta, int64_t d_out, int64_t d_in,
+                              const void *U, const void *V, int64_t r, void *dX, void *workspace, size_t workspace_bytes,
+                              slr_stream_t stream) {
+    if (M < 0 || d_out < 8 || d_out % 8 != 0 || d_in < 128 || d_in % 128 != 0 || r < 0 || r > 256 || r % 8 != 0 ||
+        M > INT32_MAX || d_out > INT32_MAX || d_in > INT32_MAX)
+        return SLR_ERR_SHAPE;
+    if (M == 0) return SLR_OK;
+    const size_t need = slr_input_backward_workspace_size(M, d_out, d_in, r);
+    if (dY == nullptr || vals == nullptr || meta == nullptr || dX == nullptr || (need > 0 && workspace == nullptr) ||
+        (r > 0 && (U == nullptr || V == nullptr)))
+        return SLR_ERR_NULL;
+    if (!slr::aligned16(dY) || !slr::aligned16(vals) || !slr::aligned16(meta) || !slr::aligned16(dX) ||
+        (r > 0 && (!slr::aligned16(U) || !slr::aligned16(V))) ||
+        (need > 0 && (reinterpret_cast<uintptr_t>(workspace) % slr::kAlign) != 0))
+        return SLR_ERR_ALIGN;
+    if (workspace_bytes < need) return SLR_ERR_WORKSPACE;
+    const slr_status dev = slr::check_device();
+    if (dev != SLR_OK) return dev;
+    const cudaError_t err = slr::launch_input_backward(
+        static_cast<const uint16_t *>(dY), M, static_cast<const uint16_t *>(vals), static_cast<const uint8_t *>(meta),
+        d_out, d_in, static_cast<const uint16_t *>(U), static_cast<const uint16_t *>(V), r, static_cast<uint16_t *>(dX),
+        static_cast<uint8_t *>(workspace), slr::current_sms(), reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? SLR_OK : SLR_ERR_CUDA;
 }
 

@@ -109,3 +109,23 @@ def test_epilogue_backward_argument_errors():
     if not torch.cuda.is_available():
         assert f(dy, z, 8, 16, 2, dz, None, None) == DEVICE and f(dy, None, 8, 16, 0, None, db, None) == DEVICE
         assert f(None, None, 0, 16, 2, None, db, None) == DEVICE
+
+
+def test_input_backward_argument_errors_and_workspace():
+    f, size = slr.lib().slr_input_backward, slr.input_backward_workspace_size
+    dy, v, m, u, vv, dx, ws = (P(0x10000 * k) for k in range(1, 8))
+    big = 1 << 40
+    assert f(None, 0, None, None, 16, 128, None, None, 0, None, None, 0, None) == OK
+    assert f(dy, -1, v, m, 16, 128, u, vv, 8, dx, ws, big, None) == SHAPE
+    for d_out, d_in, r in ((12, 128, 8), (0, 128, 8), (16, 64, 8), (16, 192, 8), (16, 128, 12), (16, 128, 264)):
+        assert f(dy, 4, v, m, d_out, d_in, u, vv, r, dx, ws, big, None) == SHAPE
+    assert f(None, 4, v, m, 16, 128, u, vv, 8, dx, ws, big, None) == NULL and f(dy, 4, v, m, 16, 128, None, vv, 8, dx, ws, big, None) == NULL
+    assert f(dy, 4, v, m, 16, 128, u, vv, 8, None, ws, big, None) == NULL and f(dy, 4, v, m, 16, 128, u, vv, 8, dx, None, big, None) == NULL
+    assert f(P(0x10008), 4, v, m, 16, 128, u, vv, 8, dx, ws, big, None) == ALIGN and f(dy, 4, v, m, 16, 128, u, vv, 8, dx, P(0x70010), big, None) == ALIGN
+    assert f(dy, 4, v, m, 16, 128, u, vv, 8, dx, ws, 16, None) == WORKSPACE
+    assert size(0, 16, 128, 8) == 0 and size(4, 16, 128, 8) >= 4 * 8 * 2 and size(4, 16, 100, 8) == 0
+    assert size(4, 16, 128, 0) == 0                                # one slice, no G
+    assert size(64, 4096, 4096, 0) % (64 * 4096 * 4) == 0          # partial tiles of the slices
+    if not torch.cuda.is_available():
+        assert f(dy, 4, v, m, 16, 128, u, vv, 8, dx, ws, big, None) == DEVICE
+        assert f(dy, 4, v, m, 16, 128, None, None, 0, dx, None, 0, None) == DEVICE
