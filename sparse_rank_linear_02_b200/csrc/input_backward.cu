@@ -22,9 +22,10 @@
 //   warp 0       TMA producer (dY; V and G),
 //   warp 1       MMA issue (leader CTA),
 //   warps 2..5   epilogue: TMEM -> bf16 -> shared memory -> TMA store,
-//   warps 6..13  expanders: a thread loads 16 bytes of kept values (four groups)
-//                and their two metadata bytes straight into registers, four
-//                stages ahead, and writes 32 bytes of the dense tile in the
+//   warps 6..13  expanders, four groups of two warps that take the stages in
+//                turn: a thread loads 16 bytes of kept values (four groups of
+//                S) and their two metadata bytes straight into registers, one
+//                turn ahead, and writes 32 bytes of the dense tile in the
 //                128-byte swizzle.  The byte permutes that place two values
 //                among four positions take their selectors from arithmetic: the
 //                selector of position p is byte p of 0x44444444 (zero), turned
@@ -72,11 +73,11 @@ constexpr int kNS = 6;
 constexpr int kOutBytes = 32 * kCols * 2;     // 32 tokens x 128 columns
 constexpr int kOutOff = kNS * kStage;
 constexpr int kBarOff = kOutOff + 2 * kOutBytes;
-constexpr int kXWarps = 8;                    // expander warps
+constexpr int kGroups = 4, kGWarps = 2;       // expander groups, which take the stages in turn, and their warps
+constexpr int kGRows = 64 / (kGWarps * 4);    // K rows of a stage per expander thread
 constexpr int kSigOff = kBarOff + 256;        // landing places of the follower's signals, and their source
-constexpr int kDxSmem = kSigOff + 16 * (kNS * kXWarps + 1) + 1024;
-constexpr int kDxThreads = (6 + kXWarps) * 32;
-constexpr int kAhead = 4;                     // stages of S in an expander's registers
+constexpr int kDxSmem = kSigOff + 16 * (kNS * kGWarps + 1) + 1024;
+constexpr int kDxThreads = (6 + kGroups * kGWarps) * 32;
 static_assert(kDxSmem <= 232448, "shared memory budget");
 
 struct DxMaps {
@@ -151,7 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kNS; ++s) {
             mbar_init(&bfull[s], 1);
-            mbar_init(&afull[s], kXWarps);
+            mbar_init(&afull[s], kGWarps);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -325,16 +326,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
         // ------------------------------------------------------------ expanders (each CTA, its 128 columns)
         // Eight consecutive threads write two K rows (k, k + 1) of one 64-column
         // panel: their 16-byte stores fall into eight different bank groups.
-        const int e = (int)threadIdx.x - 192, xw = warp - 6;
-        const int krow = (e >> 4) * 2 + ((e >> 2) & 1);              // and krow + 32
+        const int grp = (warp - 6) / kGWarps, gw = (warp - 6) % kGWarps;
+        const int e = gw * 32 + lane;
+        const int krow = (e >> 4) * 2 + ((e >> 2) & 1);              // and every 4 * kGWarps rows after it
         const int col = ((e >> 3) & 1) * 64 + (e & 3) * 16;
         const uint32_t off = (uint32_t)(((e >> 3) & 1) * (kABytes / 2) + krow * 128);
         const uint32_t c0 = off + (uint32_t)((((e & 3) * 2) ^ (krow & 7)) * 16);
         const uint32_t c1 = off + (uint32_t)((((e & 3) * 2 + 1) ^ (krow & 7)) * 16);
         const uint32_t afull0 = mapa_shared(smem_u32(&afull[0]), 0), sig0 = mapa_shared(smem_u32(signals), 0);
-        const uint32_t sig_src = smem_u32(signals + 16 * kNS * kXWarps);
+        const uint32_t sig_src = smem_u32(signals + 16 * kNS * kGWarps);
         const int64_t vld = p.d_in / 2, mld = p.d_in / 8;
-        uint32_t s = 0, ph = 0;
+        // Stage number `pos` of the pair's sequence sits in slot pos % kNS and
+        // belongs to group pos % kGroups.  A group waits for every slot of its
+        // turns, rank stages too: a skipped phase could be taken for the next.
+        uint32_t pos = 0;    // of the item's first stage
         bool ok = true;
         for (int w = pair; w < p.items && ok; w += npairs) {
             const DxItem it(p, w);
@@ -342,61 +347,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
             const bool in = d < p.d_in;
             const uint16_t *vp = p.vals + (int64_t)krow * vld + d / 2;
             const uint8_t *mp = p.meta + (int64_t)krow * mld + d / 8;
-            uint4 v[kAhead][2];
-            uint32_t m[kAhead][2];
-            auto load = [&](int b, int i) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t k = (int64_t)i * kK + 32 * h;
-                    v[b][h] = make_uint4(0, 0, 0, 0);
-                    m[b][h] = 0x4444u;   // a valid pattern for the zeros
-                    if (in && i < it.k1 && k + krow < p.d_out) {
-                        v[b][h] = ld_stream_v4(vp + k * vld);
-                        m[b][h] = __ldg(reinterpret_cast<const unsigned short *>(mp + k * mld));
-                    }
+            uint4 v[kGRows];
+            uint32_t m[kGRows];
+            auto load = [&](int h, int i) {
+                const int64_t k = (int64_t)i * kK + 4 * kGWarps * h;
+                v[h] = make_uint4(0, 0, 0, 0);
+                m[h] = 0x4444u;   // a valid pattern for the zeros
+                if (in && i < it.k1 && k + krow < p.d_out) {
+                    v[h] = ld_stream_v4(vp + k * vld);
+                    m[h] = __ldg(reinterpret_cast<const unsigned short *>(mp + k * mld));
                 }
             };
+            const int first = (int)((uint32_t)(grp - (int)pos) % kGroups), nst = it.k1 - it.k0 + it.lr;
 #pragma unroll
-            for (int b = 0; b < kAhead; ++b) load(b, it.k0 + b);
-            for (int i0 = it.k0; i0 < it.k1 && ok; i0 += kAhead) {
+            for (int h = 0; h < kGRows; ++h) load(h, it.k0 + first);
+            for (int i = first; i < nst; i += kGroups) {
+                const uint32_t at = pos + (uint32_t)i, s = at % kNS, use = at / kNS;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&empty[s], (use & 1) ^ 1))) {
+                    if (lane == 0) atomicOr(p.err, 16u);
+                    ok = false;
+                    break;
+                }
+                if (it.k0 + i >= it.k1) continue;   // a rank stage
+                uint8_t *a = smem + s * kStage;
 #pragma unroll
-                for (int b = 0; b < kAhead; ++b) {
-                    if (i0 + b >= it.k1 || !ok) break;
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&empty[s], ph ^ 1))) {
-                        if (lane == 0) atomicOr(p.err, 16u);
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *a = smem + s * kStage;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint2 g0 = expand_group(v[b][h].x, m[b][h]), g1 = expand_group(v[b][h].y, m[b][h] >> 4);
-                        const uint2 g2 = expand_group(v[b][h].z, m[b][h] >> 8), g3 = expand_group(v[b][h].w, m[b][h] >> 12);
-                        *reinterpret_cast<uint4 *>(a + c0 + h * 4096) = make_uint4(g0.x, g0.y, g1.x, g1.y);
-                        *reinterpret_cast<uint4 *>(a + c1 + h * 4096) = make_uint4(g2.x, g2.y, g3.x, g3.y);
-                    }
-                    load(b, i0 + b + kAhead);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (!leader)
-                            bulk_signal_peer(sig0 + 16 * (s * kXWarps + xw), sig_src, afull0 + s * 8);
-                        else if (xw == 0)
-                            mbar_expect_tx(&afull[s], 16 * kXWarps);
-                        else
-                            mbar_arrive(&afull[s]);
-                    }
-                    if (++s == kNS) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                for (int h = 0; h < kGRows; ++h) {
+                    const uint2 g0 = expand_group(v[h].x, m[h]), g1 = expand_group(v[h].y, m[h] >> 4);
+                    const uint2 g2 = expand_group(v[h].z, m[h] >> 8), g3 = expand_group(v[h].w, m[h] >> 12);
+                    *reinterpret_cast<uint4 *>(a + c0 + h * (4 * kGWarps * 128)) = make_uint4(g0.x, g0.y, g1.x, g1.y);
+                    *reinterpret_cast<uint4 *>(a + c1 + h * (4 * kGWarps * 128)) = make_uint4(g2.x, g2.y, g3.x, g3.y);
+                    load(h, it.k0 + i + kGroups);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (!leader)
+                        bulk_signal_peer(sig0 + 16 * (s * kGWarps + gw), sig_src, afull0 + s * 8);
+                    else if (gw == 0)
+                        mbar_expect_tx(&afull[s], 16 * kGWarps);
+                    else
+                        mbar_arrive(&afull[s]);
                 }
             }
-            for (int i = 0; i < it.lr; ++i)   // the rank stages' turns in the ring
-                if (++s == kNS) {
-                    s = 0;
-                    ph ^= 1;
-                }
+            pos += (uint32_t)nst;
         }
     }
 
