@@ -167,11 +167,11 @@ cudaError_t launch_distill_loss_grad(const uint16_t *z, int64_t M, int64_t n, in
                                      const float *t, int64_t k, float tau, const float *dloss, float *loss,
                                      uint16_t *dz, int64_t lddz, cudaStream_t stream);
 
-// dX = dY S + (dY U) V on the tensor cores (input_backward.cu).  The plan: tokens
-// per tile (a multiple of 16), token tiles, K slices; the workspace holds G =
+// dX = dY S + (dY U) V on the tensor cores (input_backward.cu).  The plan:
+// 256-column halves per tile, tokens per tile (a multiple of 16), token tiles, K slices; the workspace holds G =
 // dY U (bf16 [M, r]) and, with more than one slice, the fp32 partial tiles.
 struct DxPlan {
-    int n, ttiles, ks;
+    int halves, n, ttiles, ks;
 };
 DxPlan input_backward_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms);
 size_t input_backward_workspace(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms);

@@ -63,28 +63,52 @@ unsigned int *dx_err() {
     return addr[dev];
 }
 
-constexpr int kCols = 128;                    // input columns per CTA (half of a pair's tile)
+constexpr int kCols = 128;                    // input columns per CTA and half
 constexpr int kK = 64;                        // output rows (K) per stage
-constexpr int kMaxN = 256;                    // tokens per tile
-constexpr int kABytes = kCols * kK * 2;       // 16 KB: two 64-column panels of 64 K rows
-constexpr int kBBytes = kMaxN / 2 * kK * 2;   // 16 KB
-constexpr int kStage = kABytes + kBBytes;
-constexpr int kNS = 6;
+constexpr int kABytes = kCols * kK * 2;       // 16 KB per half: two 64-column panels of 64 K rows
 constexpr int kOutBytes = 32 * kCols * 2;     // 32 tokens x 128 columns
-constexpr int kOutOff = kNS * kStage;
-constexpr int kBarOff = kOutOff + 2 * kOutBytes;
-constexpr int kGroups = 4, kGWarps = 2;       // expander groups, which take the stages in turn, and their warps
-constexpr int kGRows = 64 / (kGWarps * 4);    // K rows of a stage per expander thread
-constexpr int kSigOff = kBarOff + 256;        // landing places of the follower's signals, and their source
-constexpr int kDxSmem = kSigOff + 16 * (kNS * kGWarps + 1) + 1024;
-constexpr int kDxThreads = (6 + kGroups * kGWarps) * 32;
-static_assert(kDxSmem <= 232448, "shared memory budget");
+constexpr int kGRows = 8;                     // K rows of a stage per expander thread, 8 apart
+constexpr int kXWarps = 8;                    // expander warps
+constexpr int kValBytes = kK * kCols;         // packed values of a stage and half: 64 rows of 128 bytes
+constexpr int kMetaTurns = 2;                 // turns that an expander warp's metadata (32 rows of 16 bytes) is ahead
+constexpr int kDxThreads = (7 + kXWarps) * 32;
+
+// H = 1: tiles of 256 columns, two accumulators of up to 256 tokens.  H = 2: two
+// such halves over the same tokens, one accumulator each of up to 240.
+template <int H>
+struct DxCfg {
+    static constexpr int MAXN = H == 1 ? 256 : 240;
+    static constexpr int B_BYTES = MAXN / 2 * kK * 2;
+    static constexpr int STAGE = H * kABytes + B_BYTES;
+    static constexpr int NS = H == 1 ? 4 : 3;
+    static constexpr int NACC = H == 1 ? 2 : 1;
+    static constexpr int GWARPS = 2 * H;              // warps of an expander group, which take the stages in turn
+    static constexpr int GROUPS = kXWarps / GWARPS;
+    static constexpr int OUT_OFF = NS * STAGE;
+    static constexpr int RAW_OFF = OUT_OFF + kOutBytes;   // ring of packed values
+    static constexpr int NR = H == 1 ? 6 : 4;
+    static constexpr int META_OFF = RAW_OFF + NR * H * kValBytes;
+    static constexpr int BAR_OFF = META_OFF + kXWarps * kMetaTurns * 512;
+    static constexpr int SIG_OFF = BAR_OFF + 256;     // landing places of the follower's signals, and their source
+    static constexpr int SMEM = SIG_OFF + 16 * (NS * GWARPS + 1) + 1024;
+    static_assert(STAGE % 1024 == 0 && B_BYTES % 1024 == 0, "swizzled tiles start on 1 KB");
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static_assert((3 * NS + 4 + 2 * NR) * 8 + 4 <= 256, "barrier area");
+    static_assert(RAW_OFF % 1024 == 0, "swizzled tiles start on 1 KB");
+    // A group's wait at its turn before (GROUPS positions back, for the slot's
+    // use NS before that) must imply the use two before the present one, or its
+    // parity could be taken for the next.
+    static_assert(GROUPS <= NS, "a wait's parity would be ambiguous");
+    // Likewise for the packed values: a group passes over the other groups' uses
+    // of a slot, but the MMAs NS positions back, which it has waited for, came
+    // after the landing of every use at least NS stages of S back.
+    static_assert(NR >= NS, "a wait's parity would be ambiguous");
+};
 
 struct DxMaps {
-    CUtensorMap dy, g, v, x32, x16;
+    CUtensorMap dy, g, v, x32, x16, vals;
 };
 struct DxParams {
-    const uint16_t *vals;
     const uint8_t *meta;
     float *part;               // [ks][M][d_in], ks > 1
     int32_t M, d_out, d_in;
@@ -95,13 +119,14 @@ struct DxParams {
 };
 
 // One tile's K slice.
+template <int H>
 struct DxItem {
     int32_t d0, tok0, k0, k1, lr, q;
     __device__ __forceinline__ DxItem(const DxParams &p, int w) {
         const int tile = w / p.ks;
         q = w - tile * p.ks;
         const int rt = tile / p.ttiles;
-        d0 = rt * 2 * kCols;
+        d0 = rt * 2 * H * kCols;
         tok0 = (tile - rt * p.ttiles) * p.n;
         k0 = (int)((int64_t)p.nk * q / p.ks);
         k1 = (int)((int64_t)p.nk * (q + 1) / p.ks);
@@ -109,11 +134,25 @@ struct DxItem {
     }
 };
 
-// Two kept values (v: low half first) at positions i0 < i1 of four, zeros
-// elsewhere; nib = i0 | i1 << 2 in the low bits.
-__device__ __forceinline__ uint2 expand_group(uint32_t v, uint32_t nib) {
-    const uint32_t sel = 0x44444444u ^ (0x54u << ((nib << 3) & 0x18u)) ^ (0x76u << ((nib << 1) & 0x18u));
-    return make_uint2(__byte_perm(v, 0, sel), __byte_perm(v, 0, sel >> 16));
+// Four groups of S from packed to dense: v holds the two kept values of each (low
+// half first), m their index nibbles i0 | i1 << 2; out the 16 columns.
+//
+// A byte permute of (v, 0) with selector byte pair 0x10 (first value), 0x32
+// (second) or 0x44 (zero) for each position places a group's values, so the work
+// is in finding the selectors, for four groups at once: the six valid nibbles
+// have different low three bits in Gray code (n ^ n >> 1: (0,1) 6, (0,2) 4,
+// (1,2) 5, (0,3) 2, (1,3) 3, (2,3) 1), which one permute per position looks up
+// in a table of eight bytes, one byte per group.  22 operations for 16 columns;
+// selectors by shifts and exclusive ors took 46 and bound the kernel (205 us
+// where 154 remained without them; integer operations issue at half rate).
+__device__ __forceinline__ void expand4(const uint4 &v, uint32_t m, uint4 &lo, uint4 &hi) {
+    const uint32_t g = (m ^ (m >> 1)) & 0x7777u;
+    const uint32_t p0 = __byte_perm(0x44104444u, 0x44104410u, g), p1 = __byte_perm(0x10444444u, 0x44321044u, g);
+    const uint32_t p2 = __byte_perm(0x44441044u, 0x44443232u, g), p3 = __byte_perm(0x32323244u, 0x44444444u, g);
+    const uint32_t a = __byte_perm(p0, p1, 0x5140), b = __byte_perm(p0, p1, 0x7362);   // positions 0, 1 of groups 0, 1; 2, 3
+    const uint32_t c = __byte_perm(p2, p3, 0x5140), d = __byte_perm(p2, p3, 0x7362);   // positions 2, 3
+    lo = make_uint4(__byte_perm(v.x, 0, a), __byte_perm(v.x, 0, c), __byte_perm(v.y, 0, a >> 16), __byte_perm(v.y, 0, c >> 16));
+    hi = make_uint4(__byte_perm(v.z, 0, b), __byte_perm(v.z, 0, d), __byte_perm(v.w, 0, b >> 16), __byte_perm(v.w, 0, d >> 16));
 }
 
 // The verdicts of a group's threads joined: all go on, or none does and no named
@@ -131,17 +170,22 @@ __device__ __forceinline__ bool group_and(uint32_t id, uint32_t n, bool ok) {
     return all != 0;
 }
 
+template <int H>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
     input_backward_kernel(const __grid_constant__ DxMaps maps, const __grid_constant__ DxParams p) {
+    using C = DxCfg<H>;
+    using Item = DxItem<H>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bfull = reinterpret_cast<uint64_t *>(smem + kBarOff);   // leader: both CTAs' TMA bytes of a stage
-    uint64_t *afull = bfull + kNS;       // leader: its expanders and the follower's signals
-    uint64_t *empty = afull + kNS;       // the stage's MMAs are done (both CTAs)
-    uint64_t *acc_full = empty + kNS;
+    uint64_t *bfull = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);   // leader: both CTAs' TMA bytes of a stage
+    uint64_t *afull = bfull + C::NS;       // leader: its expanders and the follower's signals
+    uint64_t *empty = afull + C::NS;       // the stage's MMAs are done (both CTAs)
+    uint64_t *acc_full = empty + C::NS;
     uint64_t *acc_empty = acc_full + 2;  // leader: drained by both CTAs' epilogues
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
-    uint8_t *signals = smem + kSigOff;
+    uint64_t *raw_full = acc_empty + 2;  // packed values landed / read by the group's warps (each CTA)
+    uint64_t *raw_empty = raw_full + C::NR;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_empty + C::NR);
+    uint8_t *signals = smem + C::SIG_OFF;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -150,14 +194,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
     const int half = p.n / 2;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kNS; ++s) {
+        for (int s = 0; s < C::NS; ++s) {
             mbar_init(&bfull[s], 1);
-            mbar_init(&afull[s], kGWarps);
+            mbar_init(&afull[s], C::GWARPS);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 8);
+        }
+        for (int s = 0; s < C::NR; ++s) {
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], C::GWARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -178,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
         uint32_t s = 0, ph = 0;
         bool ok = true, g_ready = false;
         for (int w = pair; w < p.items && ok; w += npairs) {
-            const DxItem it(p, w);
+            const Item it(p, w);
             const int tok = it.tok0 + (int)rank * half, d0 = it.d0 + (int)rank * kCols;
             for (int i = it.k0; i < it.k1 + it.lr; ++i) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&empty[s], ph ^ 1))) {
@@ -186,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                     ok = false;
                     break;
                 }
-                const uint32_t a = smem_u32(smem + s * kStage), b = a + kABytes, bar = bar0 + s * 8;
+                const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + H * kABytes, bar = bar0 + s * 8;
                 if (i >= it.k1 && !g_ready) {
                     asm volatile("griddepcontrol.wait;" ::: "memory");   // G may still be in production
                     g_ready = true;
@@ -197,14 +245,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                         tma_load_2d_pair(&maps.dy, b, bar, i * kK, tok);
                     } else {
                         const int j = (i - it.k1) * kK;
-                        if (leader) mbar_expect_tx(&bfull[s], (uint32_t)p.n * 128u + 2u * kABytes);
-                        tma_load_2d_pair(&maps.v, a, bar, d0, j);
-                        tma_load_2d_pair(&maps.v, a + kABytes / 2, bar, d0 + 64, j);
+                        if (leader) mbar_expect_tx(&bfull[s], (uint32_t)p.n * 128u + 2u * H * kABytes);
+#pragma unroll
+                        for (int h = 0; h < 2 * H; ++h)   // 64-column panels, two to a half
+                            tma_load_2d_pair(&maps.v, a + h * (kABytes / 2), bar, d0 + (h >> 1) * 2 * kCols + (h & 1) * 64, j);
                         tma_load_2d_pair(&maps.g, b, bar, j, tok);
                     }
                 }
                 __syncwarp();
-                if (++s == kNS) {
+                if (++s == C::NS) {
                     s = 0;
                     ph ^= 1;
                 }
@@ -218,15 +267,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
             int t = 0;
             bool ok = true;
             for (int w = pair; w < p.items && ok; w += npairs, ++t) {
-                const DxItem it(p, w);
-                const int buf = t & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_empty[buf], (uint32_t)(((t >> 1) & 1) ^ 1)));
+                const Item it(p, w);
+                const int buf = C::NACC == 2 ? t & 1 : 0;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_empty[buf], (uint32_t)((t / C::NACC & 1) ^ 1)));
                 if (!ok) {
                     if (lane == 0) atomicOr(p.err, 2u);
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(buf * kMaxN);
+                const uint32_t d = tmem_base + (uint32_t)(buf * C::MAXN);
                 for (int i = it.k0; i < it.k1 + it.lr; ++i) {
                     bool got = mbar_wait_cluster(&bfull[s], ph);
                     if (got && i < it.k1) got = mbar_wait_cluster(&afull[s], (aph >> s) & 1u);
@@ -236,16 +285,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                     }
                     if (i < it.k1) aph ^= 1u << s;
                     tc_fence_after();
-                    const uint32_t a = smem_u32(smem + s * kStage), b = a + kABytes;
+                    const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + H * kABytes;
                     if (elect_one()) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)   // K = 16 each: two 8-row groups of A, 32 bytes along B's rows
-                            mma_dense_pair(d, desc_mn_sw128(a + 2048 * c), desc_sw128(b + 32 * c), idesc,
-                                           (i > it.k0 || c > 0) ? 1u : 0u);
+                        for (int h = 0; h < H; ++h)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)   // K = 16 each: two 8-row groups of A, 32 bytes along B's rows
+                                mma_dense_pair(d + h * C::MAXN, desc_mn_sw128(a + h * kABytes + 2048 * c),
+                                               desc_sw128(b + 32 * c), idesc, (i > it.k0 || c > 0) ? 1u : 0u);
                         mma_commit_pair(&empty[s]);
                     }
                     __syncwarp();
-                    if (++s == kNS) {
+                    if (++s == C::NS) {
                         s = 0;
                         ph ^= 1;
                     }
@@ -264,33 +315,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
         const int row = quarter * 32 + lane;   // input column within the CTA's tile
         const bool store_thread = warp == 2 && lane == 0;
         const uint32_t empty0 = mapa_shared(smem_u32(&acc_empty[0]), 0);
-        uint32_t piece = 0;
         int t = 0;
         for (int w = pair; w < p.items; w += npairs, ++t) {
-            const DxItem it(p, w);
-            const int d0 = it.d0 + (int)rank * kCols;
-            const int buf = t & 1;
-            const bool ok = group_and(1, 128, mbar_wait_cluster(&acc_full[buf], (uint32_t)((t >> 1) & 1)));
+            const Item it(p, w);
+            const int buf = C::NACC == 2 ? t & 1 : 0;
+            const bool ok = group_and(1, 128, mbar_wait_cluster(&acc_full[buf], (uint32_t)(t / C::NACC & 1)));
             if (!ok) {
                 if (lane == 0) atomicOr(p.err, 8u);
                 break;
             }
             tc_fence_after();
-            const uint32_t acc = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * kMaxN);
             const int nq = (p.n + 31) / 32;
 #pragma unroll 1
-            for (int q = 0; q < nq; ++q) {
+            for (int hq = 0; hq < H * nq; ++hq) {
+                const int h = hq < nq ? 0 : 1, q = hq - h * nq;
+                const int d0 = it.d0 + h * 2 * kCols + (int)rank * kCols;
+                const uint32_t acc = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)((buf + h) * C::MAXN);
                 const bool wide = p.n - q * 32 >= 32;   // else a last piece of 16 tokens
                 uint32_t v[32];
                 if (wide) {
                     tmem_ld_32x32b_x32(acc + (uint32_t)(q * 32), v);
                 } else {
-                    uint32_t h[16];
-                    tmem_ld_32x32b_x16(acc + (uint32_t)(q * 32), h);
+                    uint32_t u[16];
+                    tmem_ld_32x32b_x16(acc + (uint32_t)(q * 32), u);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = h[j];
+                    for (int j = 0; j < 16; ++j) v[j] = u[j];
                 }
-                if (q == nq - 1) {
+                if (hq == H * nq - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_relaxed(empty0 + (uint32_t)(buf * 8));
@@ -306,9 +357,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                     }
                     continue;
                 }
-                if (store_thread) bulk_wait_read1();
+                if (store_thread) bulk_wait_read0();
                 named_bar_sync(2, 128);
-                uint16_t *out = reinterpret_cast<uint16_t *>(smem + kOutOff + (piece & 1) * kOutBytes);
+                uint16_t *out = reinterpret_cast<uint16_t *>(smem + C::OUT_OFF);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if (wide || j < 16) out[j * kCols + row] = f32_to_bf16_bits(__uint_as_float(v[j]));
@@ -318,78 +369,135 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                     tma_store_2d(wide ? &maps.x32 : &maps.x16, smem_u32(out), d0, tq);
                     bulk_commit();
                 }
-                ++piece;
             }
         }
         if (store_thread) bulk_wait_all();
-    } else {
-        // ------------------------------------------------------------ expanders (each CTA, its 128 columns)
-        // Eight consecutive threads write two K rows (k, k + 1) of one 64-column
-        // panel: their 16-byte stores fall into eight different bank groups.
-        const int grp = (warp - 6) / kGWarps, gw = (warp - 6) % kGWarps;
-        const int e = gw * 32 + lane;
-        const int krow = (e >> 4) * 2 + ((e >> 2) & 1);              // and every 4 * kGWarps rows after it
-        const int col = ((e >> 3) & 1) * 64 + (e & 3) * 16;
-        const uint32_t off = (uint32_t)(((e >> 3) & 1) * (kABytes / 2) + krow * 128);
-        const uint32_t c0 = off + (uint32_t)((((e & 3) * 2) ^ (krow & 7)) * 16);
-        const uint32_t c1 = off + (uint32_t)((((e & 3) * 2 + 1) ^ (krow & 7)) * 16);
-        const uint32_t afull0 = mapa_shared(smem_u32(&afull[0]), 0), sig0 = mapa_shared(smem_u32(signals), 0);
-        const uint32_t sig_src = smem_u32(signals + 16 * kNS * kGWarps);
-        const int64_t vld = p.d_in / 2, mld = p.d_in / 8;
-        // Stage number `pos` of the pair's sequence sits in slot pos % kNS and
-        // belongs to group pos % kGroups.  A group waits for every slot of its
-        // turns, rank stages too: a skipped phase could be taken for the next.
-        uint32_t pos = 0;    // of the item's first stage
+    } else if (warp == 6 + kXWarps) {
+        // ------------------------------------------------------------ packed values (each CTA)
+        uint32_t s = 0, ph = 0;
         bool ok = true;
         for (int w = pair; w < p.items && ok; w += npairs) {
-            const DxItem it(p, w);
-            const int d = it.d0 + (int)rank * kCols + col;
-            const bool in = d < p.d_in;
-            const uint16_t *vp = p.vals + (int64_t)krow * vld + d / 2;
-            const uint8_t *mp = p.meta + (int64_t)krow * mld + d / 8;
-            uint4 v[kGRows];
-            uint32_t m[kGRows];
-            auto load = [&](int h, int i) {
-                const int64_t k = (int64_t)i * kK + 4 * kGWarps * h;
-                v[h] = make_uint4(0, 0, 0, 0);
-                m[h] = 0x4444u;   // a valid pattern for the zeros
-                if (in && i < it.k1 && k + krow < p.d_out) {
-                    v[h] = ld_stream_v4(vp + k * vld);
-                    m[h] = __ldg(reinterpret_cast<const unsigned short *>(mp + k * mld));
+            const Item it(p, w);
+            const int d0 = it.d0 + (int)rank * kCols;
+            for (int i = it.k0; i < it.k1; ++i) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&raw_empty[s], ph ^ 1))) {
+                    if (lane == 0) atomicOr(p.err, 32u);
+                    ok = false;
+                    break;
                 }
-            };
-            const int first = (int)((uint32_t)(grp - (int)pos) % kGroups), nst = it.k1 - it.k0 + it.lr;
+                if (elect_one()) {
+                    mbar_expect_tx(&raw_full[s], H * kValBytes);
 #pragma unroll
-            for (int h = 0; h < kGRows; ++h) load(h, it.k0 + first);
-            for (int i = first; i < nst; i += kGroups) {
-                const uint32_t at = pos + (uint32_t)i, s = at % kNS, use = at / kNS;
+                    for (int h = 0; h < H; ++h)
+                        tma_load_2d(&maps.vals, smem_u32(smem + C::RAW_OFF + (s * H + h) * kValBytes), &raw_full[s],
+                                    (d0 + h * 2 * kCols) / 2, i * kK);
+                }
+                __syncwarp();
+                if (++s == C::NR) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ expanders (each CTA, its 128 columns)
+        // A thread's 16 bytes of row k of the packed tile become two 16-byte pieces
+        // of row k of the dense one, both in the 128-byte swizzle.  Eight
+        // consecutive threads take rows k and k ^ 5 of one 64-column panel: bit 2
+        // tells their reads apart, bit 0 their writes, so that each falls into
+        // eight different bank groups.
+        const int grp = (warp - 6) / C::GWARPS, gw = (warp - 6) % C::GWARPS;
+        const int mine = ((lane >> 4) & 1) + (gw & 1) * 2;           // the pair of rows, of eight
+        const int krow = ((lane >> 2) & 1) ? mine ^ 5 : mine;        // and every eighth row after it
+        const int panel = (lane >> 3) & 1, quad = lane & 3;
+        const int hcol = (gw >> 1) * 2 * kCols;                      // the warp's half
+        const uint32_t off = (uint32_t)((gw >> 1) * kABytes + panel * (kABytes / 2) + krow * 128);
+        const uint32_t c0 = off + (uint32_t)(((quad * 2) ^ krow) * 16);
+        const uint32_t c1 = off + (uint32_t)(((quad * 2 + 1) ^ krow) * 16);
+        const uint32_t rv = (uint32_t)((gw >> 1) * kValBytes + krow * 128 + (((panel * 4 + quad) ^ krow) * 16));
+        // The warp's metadata come by cp.async, 16 bytes a lane: K row
+        // `mrow(lane)`, the lanes of a row pair in the pairs' order.  (As TMA boxes
+        // the 16-byte rows would cost as much as the 128-byte rows of the values;
+        // two-byte loads into registers, and all of S by 16-byte loads, held the
+        // SM's intake to 52 GB/s, where TMA takes in 66.)
+        uint8_t *meta0 = smem + C::META_OFF + (warp - 6) * (kMetaTurns * 512);
+        const int mpair = ((lane >> 1) & 1) + (gw & 1) * 2;
+        const int mrow = ((lane & 1) ? mpair ^ 5 : mpair) + 8 * (lane >> 2);
+        const uint32_t rm = (uint32_t)((((lane >> 4) & 1) * 2 + ((lane >> 2) & 1)) * 16 + panel * 8 + quad * 2);
+        const uint32_t afull0 = mapa_shared(smem_u32(&afull[0]), 0), sig0 = mapa_shared(smem_u32(signals), 0);
+        const uint32_t sig_src = smem_u32(signals + 16 * C::NS * C::GWARPS);
+        const int64_t mld = p.d_in / 8;
+        // Stage number `pos` of the pair's sequence sits in slot pos % NS and
+        // belongs to group pos % GROUPS.  A group waits for every slot of its
+        // turns, rank stages too: a skipped phase could be taken for the next.
+        uint32_t pos = 0;    // of the item's first stage
+        uint32_t rpos = 0;   // its number among the stages of S: the packed values' ring
+        bool ok = true;
+        for (int w = pair; w < p.items && ok; w += npairs) {
+            const Item it(p, w);
+            const int d = it.d0 + (int)rank * kCols + hcol;
+            const bool in = d < p.d_in;
+            // Rows past d_out and stages past the slice come as zeros, which place
+            // zeros.
+            auto copy = [&](int b, int i) {
+                if (i < it.k1) {
+                    const int64_t k = (int64_t)i * kK + mrow;
+                    const bool there = in && k < p.d_out;
+                    const uint8_t *src = there ? p.meta + k * mld + d / 8 : p.meta;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(meta0 + b * 512 + lane * 16)),
+                                 "l"(src), "r"(there ? 16 : 0)
+                                 : "memory");
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            const int first = (int)((uint32_t)(grp - (int)pos) % C::GROUPS), nst = it.k1 - it.k0 + it.lr;
+            int b = 0;
+#pragma unroll
+            for (int t = 0; t < kMetaTurns; ++t) copy(t, it.k0 + first + t * C::GROUPS);
+            for (int i = first; i < nst; i += C::GROUPS) {
+                const uint32_t at = pos + (uint32_t)i, s = at % C::NS, use = at / C::NS;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&empty[s], (use & 1) ^ 1))) {
                     if (lane == 0) atomicOr(p.err, 16u);
                     ok = false;
                     break;
                 }
                 if (it.k0 + i >= it.k1) continue;   // a rank stage
-                uint8_t *a = smem + s * kStage;
+                asm volatile("cp.async.wait_group %0;" ::"n"(kMetaTurns - 1) : "memory");
+                const uint32_t rat = rpos + (uint32_t)i, rs = rat % C::NR;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&raw_full[rs], (rat / C::NR) & 1))) {
+                    if (lane == 0) atomicOr(p.err, 64u);
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                uint8_t *a = smem + s * C::STAGE;
+                const uint8_t *raw = smem + C::RAW_OFF + rs * (H * kValBytes), *meta = meta0 + b * 512;
 #pragma unroll
                 for (int h = 0; h < kGRows; ++h) {
-                    const uint2 g0 = expand_group(v[h].x, m[h]), g1 = expand_group(v[h].y, m[h] >> 4);
-                    const uint2 g2 = expand_group(v[h].z, m[h] >> 8), g3 = expand_group(v[h].w, m[h] >> 12);
-                    *reinterpret_cast<uint4 *>(a + c0 + h * (4 * kGWarps * 128)) = make_uint4(g0.x, g0.y, g1.x, g1.y);
-                    *reinterpret_cast<uint4 *>(a + c1 + h * (4 * kGWarps * 128)) = make_uint4(g2.x, g2.y, g3.x, g3.y);
-                    load(h, it.k0 + i + kGroups);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(raw + rv + h * 1024);
+                    const uint32_t m = *reinterpret_cast<const uint16_t *>(meta + rm + h * 64);
+                    uint4 lo, hi;
+                    expand4(v, m, lo, hi);
+                    *reinterpret_cast<uint4 *>(a + c0 + h * 1024) = lo;
+                    *reinterpret_cast<uint4 *>(a + c1 + h * 1024) = hi;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
+                    mbar_arrive(&raw_empty[rs]);
                     if (!leader)
-                        bulk_signal_peer(sig0 + 16 * (s * kGWarps + gw), sig_src, afull0 + s * 8);
+                        bulk_signal_peer(sig0 + 16 * (s * C::GWARPS + gw), sig_src, afull0 + s * 8);
                     else if (gw == 0)
-                        mbar_expect_tx(&afull[s], 16 * kGWarps);
+                        mbar_expect_tx(&afull[s], 16 * C::GWARPS);
                     else
                         mbar_arrive(&afull[s]);
                 }
+                copy(b, it.k0 + i + kMetaTurns * C::GROUPS);
+                b = b + 1 == kMetaTurns ? 0 : b + 1;
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
             pos += (uint32_t)nst;
+            rpos += (uint32_t)(it.k1 - it.k0);
         }
     }
 
@@ -423,28 +531,32 @@ __global__ void __launch_bounds__(256) input_backward_sum_kernel(const float *__
 
 }  // namespace
 
-// Tokens per tile and K slices for a problem, by the estimated cycles of the
-// busiest pair: rounds of tiles x stages, a stage at the larger of its MMAs (2 n
-// cycles), its bytes at the 44 a cycle that an SM takes in, and the expanders
-// (~240); a slice's partial tile and the second kernel cost extra.
+// Halves, tokens per tile and K slices for a problem, by the estimated cycles of
+// the busiest pair: rounds of tiles x stages, a stage at the larger of its MMAs
+// (2 n cycles a half) and its bytes at the 35 a cycle that an SM takes in
+// (measured: without its MMAs the kernel is hardly faster); the drain of an
+// accumulator that is not overlapped, and a slice's partial tile and the second
+// kernel, cost extra.
 DxPlan input_backward_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms) {
-    const int64_t ut = (M + 15) / 16, rows = (d_in + 255) / 256, nk = (d_out + kK - 1) / kK, nlr = (r + 63) / 64;
+    const int64_t ut = (M + 15) / 16, nk = (d_out + kK - 1) / kK, nlr = (r + 63) / 64;
     const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
-    DxPlan best{0, 0, 1};
+    DxPlan best{1, 0, 0, 1};
     double best_cost = 0;
-    const int64_t tmin = (ut + kMaxN / 16 - 1) / (kMaxN / 16);
-    for (int64_t tt = tmin; tt <= tmin + 6 && tt <= ut; ++tt) {
-        const int64_t nu = (ut + tt - 1) / tt, ttiles = (ut + nu - 1) / nu;
-        const double n = 16.0 * nu, bytes = (9216.0 + 64.0 * n) / 44.0;
-        double stage = 2.0 * n > bytes ? 2.0 * n : bytes;
-        if (stage < 240.0) stage = 240.0;
-        for (int64_t ks = 1; ks <= 8 && ks * 4 <= nk + 3; ++ks) {
-            const int64_t rounds = (rows * ttiles * ks + pairs - 1) / pairs;
-            double cost = rounds * (((nk + ks - 1) / ks + nlr) * stage + 1500.0);
-            if (ks > 1) cost += 5000.0 + (double)ks * M * d_in * 8.0 / (pairs * 40.0);
-            if (best.n == 0 || cost < best_cost) {
-                best = DxPlan{(int)(16 * nu), (int)ttiles, (int)ks};
-                best_cost = cost;
+    for (int h = 1; h <= 2; ++h) {
+        const int64_t rows = (d_in + 256 * h - 1) / (256 * h), chu = (h == 1 ? DxCfg<1>::MAXN : DxCfg<2>::MAXN) / 16;
+        const int64_t tmin = (ut + chu - 1) / chu;
+        for (int64_t tt = tmin; tt <= tmin + 6 && tt <= ut; ++tt) {
+            const int64_t nu = (ut + tt - 1) / tt, ttiles = (ut + nu - 1) / nu;
+            const double n = 16.0 * nu, bytes = (9216.0 * h + 64.0 * n) / 35.0;
+            const double stage = 2.0 * n * h > bytes ? 2.0 * n * h : bytes;
+            for (int64_t ks = 1; ks <= 8 && ks * 4 <= nk + 3; ++ks) {
+                const int64_t rounds = (rows * ttiles * ks + pairs - 1) / pairs;
+                double cost = rounds * (((nk + ks - 1) / ks + nlr) * stage + (h == 1 ? 1500.0 : 1500.0 + 18.0 * n));
+                if (ks > 1) cost += 5000.0 + (double)ks * M * d_in * 8.0 / (pairs * 40.0);
+                if (best.n == 0 || cost < best_cost) {
+                    best = DxPlan{h, (int)(16 * nu), (int)ttiles, (int)ks};
+                    best_cost = cost;
+                }
             }
         }
     }
@@ -477,6 +589,7 @@ cudaError_t launch_input_backward(const uint16_t *dY, int64_t M, const uint16_t 
     DxMaps maps;
     memset(&maps, 0, sizeof maps);
     bool ok = make_map(&maps.dy, kBF16, dY, d_out, M, d_out * 2, 64, plan.n / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
+              make_map(&maps.vals, kBF16, vals, d_in / 2, d_out, d_in, 64, kK, CU_TENSOR_MAP_SWIZZLE_128B) &&
               make_map(&maps.x32, kBF16, dX, d_in, M, d_in * 2, kCols, 32, CU_TENSOR_MAP_SWIZZLE_NONE) &&
               make_map(&maps.x16, kBF16, dX, d_in, M, d_in * 2, kCols, 16, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (ok && r > 0)
@@ -484,7 +597,6 @@ cudaError_t launch_input_backward(const uint16_t *dY, int64_t M, const uint16_t 
              make_map(&maps.v, kBF16, V, d_in, r, d_in * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return cudaErrorInvalidValue;
     DxParams p;
-    p.vals = vals;
     p.meta = meta;
     p.part = reinterpret_cast<float *>(ws + ((size_t)M * (size_t)r * 2 + 255) / 256 * 256);
     p.M = (int32_t)M;
@@ -495,25 +607,26 @@ cudaError_t launch_input_backward(const uint16_t *dY, int64_t M, const uint16_t 
     p.n = plan.n;
     p.ttiles = plan.ttiles;
     p.ks = plan.ks;
-    const int64_t items = (d_in + 255) / 256 * plan.ttiles * plan.ks;
+    const int64_t items = (d_in + 256 * plan.halves - 1) / (256 * plan.halves) * plan.ttiles * plan.ks;
     if (items > INT32_MAX) return cudaErrorInvalidValue;
     p.items = (int32_t)items;
     p.err = dx_err();
-    cudaError_t err =
-        cudaFuncSetAttribute(input_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDxSmem);
+    const auto kernel = plan.halves == 1 ? input_backward_kernel<1> : input_backward_kernel<2>;
+    const int smem = plan.halves == 1 ? DxCfg<1>::SMEM : DxCfg<2>::SMEM;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     const int64_t pairs = items < sms / 2 ? items : sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(kDxThreads);
-    cfg.dynamicSmemBytes = kDxSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = r > 0 ? 1 : 0;   // the kernel just before is the one that writes G
-    err = cudaLaunchKernelEx(&cfg, input_backward_kernel, maps, p);
+    err = cudaLaunchKernelEx(&cfg, kernel, maps, p);
     if (err != cudaSuccess || plan.ks == 1) return err;
     const int64_t total = M * d_in;
     cfg.gridDim = dim3((unsigned)((total + 1023) / 1024));
