@@ -11,28 +11,34 @@
 //                 contiguous along d_in, as tcgen05 reads it with the operand's
 //                 major-ness in the instruction descriptor,
 //   B = dY tile   n tokens x 64 K, K-major, by TMA,
-//   D = dX^T tile 256 x n fp32 in TMEM, two accumulators of up to 256 columns.
+//   D = dX^T tile 256 x n fp32 in TMEM: two accumulators of up to 256 tokens, or
+//                 two 256-column halves over the same tokens (up to 240), which
+//                 read the dY tile once for twice the MMAs.
 // After the d_out / 64 stages of S, ceil(r / 64) rank stages add A = V tile (64
 // ranks x 256 columns, MN-major, by TMA), B = G tile.  G is formed before by the
 // product kernel of the factors' gradients (tc_gemm.cuh) and rounded to bf16, as
-// there: the tensor cores read bf16.
+// there: the tensor cores read bf16.  This kernel starts beside it on the SMs it
+// leaves free and waits for it before the rank stages.
 //
 // A cluster of two CTAs on neighbouring SMs shares a tile (cta_group::2): each
-// expands 128 of its columns and loads half of its tokens.
+// expands its half of the columns and loads half of the tokens.
 //   warp 0       TMA producer (dY; V and G),
 //   warp 1       MMA issue (leader CTA),
-//   warps 2..5   epilogue: TMEM -> bf16 -> shared memory -> TMA store,
-//   warps 6..13  expanders, four groups of two warps that take the stages in
-//                turn: a thread loads 16 bytes of kept values (four groups of
-//                S) and their two metadata bytes straight into registers, one
-//                turn ahead, and writes 32 bytes of the dense tile in the
-//                128-byte swizzle.  The byte permutes that place two values
-//                among four positions take their selectors from arithmetic: the
-//                selector of position p is byte p of 0x44444444 (zero), turned
-//                into 0x10 (first value) or 0x32 (second) by an exclusive or.
+//   warps 2..9   epilogue: TMEM -> bf16 -> shared memory -> TMA store,
+//   warps 10..17 expanders, in groups that take the stages in turn: a thread
+//                reads 16 bytes of kept values (four groups of S) and their two
+//                metadata bytes from shared memory and writes 32 bytes of the
+//                dense tile in the 128-byte swizzle,
+//   warp 18      TMA producer of the packed values.
 // The follower's expanders announce a stage to the leader with 16-byte bulk
 // copies that complete on its barrier, since a release-ordered remote arrive
 // would stall them for most of a microsecond each.
+//
+// What bounds it: MMAs and the SM's intake of dY, values and metadata, about
+// equal (34 KB and 960 MMA cycles a stage of two halves x 240 tokens).  Measured,
+// 2048 tokens of 14336 x 4096 without the rank term: 170 us = 1410 TF/s of the
+// dense product (cuBLAS: 1670); all of S by 16-byte loads 186 us; one half 193;
+// eight warps on every stage instead of groups in turn 252.
 //
 // Few tiles (short batches): the K stages are split over the pairs that would
 // idle; slices leave fp32 partial tiles in the workspace, which a second kernel
@@ -71,7 +77,9 @@ constexpr int kGRows = 8;                     // K rows of a stage per expander 
 constexpr int kXWarps = 8;                    // expander warps
 constexpr int kValBytes = kK * kCols;         // packed values of a stage and half: 64 rows of 128 bytes
 constexpr int kMetaTurns = 2;                 // turns that an expander warp's metadata (32 rows of 16 bytes) is ahead
-constexpr int kDxThreads = (7 + kXWarps) * 32;
+constexpr int kEWarps = 8;                    // epilogue warps, two groups of four
+constexpr int kXFirst = 2 + kEWarps;          // first expander warp
+constexpr int kDxThreads = (3 + kEWarps + kXWarps) * 32;
 
 // H = 1: tiles of 256 columns, two accumulators of up to 256 tokens.  H = 2: two
 // such halves over the same tokens, one accumulator each of up to 240.
@@ -85,8 +93,8 @@ struct DxCfg {
     static constexpr int GWARPS = 2 * H;              // warps of an expander group, which take the stages in turn
     static constexpr int GROUPS = kXWarps / GWARPS;
     static constexpr int OUT_OFF = NS * STAGE;
-    static constexpr int RAW_OFF = OUT_OFF + kOutBytes;   // ring of packed values
-    static constexpr int NR = H == 1 ? 6 : 4;
+    static constexpr int RAW_OFF = OUT_OFF + 2 * kOutBytes;   // ring of packed values
+    static constexpr int NR = H == 1 ? 6 : 3;
     static constexpr int META_OFF = RAW_OFF + NR * H * kValBytes;
     static constexpr int BAR_OFF = META_OFF + kXWarps * kMetaTurns * 512;
     static constexpr int SIG_OFF = BAR_OFF + 256;     // landing places of the follower's signals, and their source
@@ -201,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], 2 * kEWarps);
         }
         for (int s = 0; s < C::NR; ++s) {
             mbar_init(&raw_full[s], 1);
@@ -309,26 +317,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp < 6) {
+    } else if (warp < kXFirst) {
         // ------------------------------------------------------------ epilogue (each CTA, its 128 columns)
-        const int quarter = warp & 3;
+        // Two groups of four warps (one per TMEM lane quarter): each drains one
+        // half, or every other piece of a tile of one half.
+        const int grp = (warp - 2) >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;   // input column within the CTA's tile
-        const bool store_thread = warp == 2 && lane == 0;
+        const bool store_thread = ((warp - 2) & 3) == 0 && lane == 0;
+        uint16_t *out = reinterpret_cast<uint16_t *>(smem + C::OUT_OFF + grp * kOutBytes);
         const uint32_t empty0 = mapa_shared(smem_u32(&acc_empty[0]), 0);
         int t = 0;
         for (int w = pair; w < p.items; w += npairs, ++t) {
             const Item it(p, w);
             const int buf = C::NACC == 2 ? t & 1 : 0;
-            const bool ok = group_and(1, 128, mbar_wait_cluster(&acc_full[buf], (uint32_t)(t / C::NACC & 1)));
+            const bool ok = group_and(1 + grp, 128, mbar_wait_cluster(&acc_full[buf], (uint32_t)(t / C::NACC & 1)));
             if (!ok) {
                 if (lane == 0) atomicOr(p.err, 8u);
                 break;
             }
             tc_fence_after();
             const int nq = (p.n + 31) / 32;
+            if (H == 1 && grp >= nq) {   // one piece: nothing for the second group
+                tc_fence_before();
+                if (lane == 0) mbar_arrive_remote_relaxed(empty0 + (uint32_t)(buf * 8));
+            }
 #pragma unroll 1
-            for (int hq = 0; hq < H * nq; ++hq) {
-                const int h = hq < nq ? 0 : 1, q = hq - h * nq;
+            for (int q = H == 1 ? grp : 0; q < nq; q += H == 1 ? 2 : 1) {
+                const int h = H == 1 ? 0 : grp;
                 const int d0 = it.d0 + h * 2 * kCols + (int)rank * kCols;
                 const uint32_t acc = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)((buf + h) * C::MAXN);
                 const bool wide = p.n - q * 32 >= 32;   // else a last piece of 16 tokens
@@ -341,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = u[j];
                 }
-                if (hq == H * nq - 1) {
+                if (q + (H == 1 ? 2 : 1) >= nq) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_relaxed(empty0 + (uint32_t)(buf * 8));
@@ -358,13 +373,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                     continue;
                 }
                 if (store_thread) bulk_wait_read0();
-                named_bar_sync(2, 128);
-                uint16_t *out = reinterpret_cast<uint16_t *>(smem + C::OUT_OFF);
+                named_bar_sync(3 + grp, 128);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if (wide || j < 16) out[j * kCols + row] = f32_to_bf16_bits(__uint_as_float(v[j]));
                 fence_proxy_async_smem();
-                named_bar_sync(2, 128);
+                named_bar_sync(3 + grp, 128);
                 if (store_thread) {
                     tma_store_2d(wide ? &maps.x32 : &maps.x16, smem_u32(out), d0, tq);
                     bulk_commit();
@@ -372,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
             }
         }
         if (store_thread) bulk_wait_all();
-    } else if (warp == 6 + kXWarps) {
+    } else if (warp == kXFirst + kXWarps) {
         // ------------------------------------------------------------ packed values (each CTA)
         uint32_t s = 0, ph = 0;
         bool ok = true;
@@ -406,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
         // consecutive threads take rows k and k ^ 5 of one 64-column panel: bit 2
         // tells their reads apart, bit 0 their writes, so that each falls into
         // eight different bank groups.
-        const int grp = (warp - 6) / C::GWARPS, gw = (warp - 6) % C::GWARPS;
+        const int grp = (warp - kXFirst) / C::GWARPS, gw = (warp - kXFirst) % C::GWARPS;
         const int mine = ((lane >> 4) & 1) + (gw & 1) * 2;           // the pair of rows, of eight
         const int krow = ((lane >> 2) & 1) ? mine ^ 5 : mine;        // and every eighth row after it
         const int panel = (lane >> 3) & 1, quad = lane & 3;
@@ -420,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
         // the 16-byte rows would cost as much as the 128-byte rows of the values;
         // two-byte loads into registers, and all of S by 16-byte loads, held the
         // SM's intake to 52 GB/s, where TMA takes in 66.)
-        uint8_t *meta0 = smem + C::META_OFF + (warp - 6) * (kMetaTurns * 512);
+        uint8_t *meta0 = smem + C::META_OFF + (warp - kXFirst) * (kMetaTurns * 512);
         const int mpair = ((lane >> 1) & 1) + (gw & 1) * 2;
         const int mrow = ((lane & 1) ? mpair ^ 5 : mpair) + 8 * (lane >> 2);
         const uint32_t rm = (uint32_t)((((lane >> 4) & 1) * 2 + ((lane >> 2) & 1)) * 16 + panel * 8 + quad * 2);

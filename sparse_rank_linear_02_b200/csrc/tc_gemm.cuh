@@ -115,6 +115,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
     volatile uint32_t *fail = tmem_slot + 1;
     float *part = reinterpret_cast<float *>(smem);  // reuses the ring after the K loop
 
+    // A kernel launched behind this one as its programmatic dependent may start
+    // on the SMs that this grid leaves free (it waits before it reads the result).
+    asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t ks_n;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ks_n));
