@@ -25,11 +25,11 @@
 //   warp 0       TMA producer (dY; V and G),
 //   warp 1       MMA issue (leader CTA),
 //   warps 2..9   epilogue: TMEM -> bf16 -> shared memory -> TMA store,
-//   warps 10..17 expanders, in groups that take the stages in turn: a thread
+//   warps 10..   expanders, in groups that take the stages in turn: a thread
 //                reads 16 bytes of kept values (four groups of S) and their two
 //                metadata bytes from shared memory and writes 32 bytes of the
 //                dense tile in the 128-byte swizzle,
-//   warp 18      TMA producer of the packed values.
+//   last warp    TMA producer of the packed values.
 // The follower's expanders announce a stage to the leader with 16-byte bulk
 // copies that complete on its barrier, since a release-ordered remote arrive
 // would stall them for most of a microsecond each.
@@ -73,13 +73,10 @@ constexpr int kCols = 128;                    // input columns per CTA and half
 constexpr int kK = 64;                        // output rows (K) per stage
 constexpr int kABytes = kCols * kK * 2;       // 16 KB per half: two 64-column panels of 64 K rows
 constexpr int kOutBytes = 32 * kCols * 2;     // 32 tokens x 128 columns
-constexpr int kGRows = 8;                     // K rows of a stage per expander thread, 8 apart
-constexpr int kXWarps = 8;                    // expander warps
 constexpr int kValBytes = kK * kCols;         // packed values of a stage and half: 64 rows of 128 bytes
 constexpr int kMetaTurns = 2;                 // turns that an expander warp's metadata (32 rows of 16 bytes) is ahead
 constexpr int kEWarps = 8;                    // epilogue warps, two groups of four
 constexpr int kXFirst = 2 + kEWarps;          // first expander warp
-constexpr int kDxThreads = (3 + kEWarps + kXWarps) * 32;
 
 // H = 1: tiles of 256 columns, two accumulators of up to 256 tokens.  H = 2: two
 // such halves over the same tokens, one accumulator each of up to 240.
@@ -90,13 +87,18 @@ struct DxCfg {
     static constexpr int STAGE = H * kABytes + B_BYTES;
     static constexpr int NS = H == 1 ? 4 : 3;
     static constexpr int NACC = H == 1 ? 2 : 1;
-    static constexpr int GWARPS = 2 * H;              // warps of an expander group, which take the stages in turn
-    static constexpr int GROUPS = kXWarps / GWARPS;
+    // Expanders: groups, which take the stages in turn, of GWARPS warps, WPH to a
+    // half; a thread has ROWS of the stage's K rows, eight apart.  (Two halves
+    // with 8 warps in all: 172 us where 16 take 166, one half with 16 warps 17.6
+    // us where 8 take 14.9 -- 2048 tokens of 14336 x 4096, 64 of 4096 x 4096, r = 0.)
+    static constexpr int WPH = 2 * H, GWARPS = WPH * H, GROUPS = H == 1 ? 4 : 2, XWARPS = GWARPS * GROUPS;
+    static constexpr int ROWS = 16 / WPH;
+    static constexpr int THREADS = (3 + kEWarps + XWARPS) * 32;
     static constexpr int OUT_OFF = NS * STAGE;
     static constexpr int RAW_OFF = OUT_OFF + 2 * kOutBytes;   // ring of packed values
     static constexpr int NR = H == 1 ? 6 : 3;
     static constexpr int META_OFF = RAW_OFF + NR * H * kValBytes;
-    static constexpr int BAR_OFF = META_OFF + kXWarps * kMetaTurns * 512;
+    static constexpr int BAR_OFF = META_OFF + XWARPS * kMetaTurns * ROWS * 64;
     static constexpr int SIG_OFF = BAR_OFF + 256;     // landing places of the follower's signals, and their source
     static constexpr int SMEM = SIG_OFF + 16 * (NS * GWARPS + 1) + 1024;
     static_assert(STAGE % 1024 == 0 && B_BYTES % 1024 == 0, "swizzled tiles start on 1 KB");
@@ -179,7 +181,7 @@ __device__ __forceinline__ bool group_and(uint32_t id, uint32_t n, bool ok) {
 }
 
 template <int H>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DxCfg<H>::THREADS, 1)
     input_backward_kernel(const __grid_constant__ DxMaps maps, const __grid_constant__ DxParams p) {
     using C = DxCfg<H>;
     using Item = DxItem<H>;
@@ -386,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
             }
         }
         if (store_thread) bulk_wait_all();
-    } else if (warp == kXFirst + kXWarps) {
+    } else if (warp == kXFirst + C::XWARPS) {
         // ------------------------------------------------------------ packed values (each CTA)
         uint32_t s = 0, ph = 0;
         bool ok = true;
@@ -424,19 +426,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
         const int mine = ((lane >> 4) & 1) + (gw & 1) * 2;           // the pair of rows, of eight
         const int krow = ((lane >> 2) & 1) ? mine ^ 5 : mine;        // and every eighth row after it
         const int panel = (lane >> 3) & 1, quad = lane & 3;
-        const int hcol = (gw >> 1) * 2 * kCols;                      // the warp's half
-        const uint32_t off = (uint32_t)((gw >> 1) * kABytes + panel * (kABytes / 2) + krow * 128);
+        const int base = C::WPH == 4 ? (gw & 2) * 16 : 0;            // four warps to a half: its first or second 32 rows
+        const int half = gw / C::WPH, hcol = half * 2 * kCols;                      // the warp's half
+        const uint32_t off = (uint32_t)(half * kABytes + panel * (kABytes / 2) + (base + krow) * 128);
         const uint32_t c0 = off + (uint32_t)(((quad * 2) ^ krow) * 16);
         const uint32_t c1 = off + (uint32_t)(((quad * 2 + 1) ^ krow) * 16);
-        const uint32_t rv = (uint32_t)((gw >> 1) * kValBytes + krow * 128 + (((panel * 4 + quad) ^ krow) * 16));
+        const uint32_t rv = (uint32_t)(half * kValBytes + (base + krow) * 128 + (((panel * 4 + quad) ^ krow) * 16));
         // The warp's metadata come by cp.async, 16 bytes a lane: K row
         // `mrow(lane)`, the lanes of a row pair in the pairs' order.  (As TMA boxes
         // the 16-byte rows would cost as much as the 128-byte rows of the values;
         // two-byte loads into registers, and all of S by 16-byte loads, held the
         // SM's intake to 52 GB/s, where TMA takes in 66.)
-        uint8_t *meta0 = smem + C::META_OFF + (warp - kXFirst) * (kMetaTurns * 512);
+        uint8_t *meta0 = smem + C::META_OFF + (warp - kXFirst) * (kMetaTurns * C::ROWS * 64);
         const int mpair = ((lane >> 1) & 1) + (gw & 1) * 2;
-        const int mrow = ((lane & 1) ? mpair ^ 5 : mpair) + 8 * (lane >> 2);
+        const int mrow = base + ((lane & 1) ? mpair ^ 5 : mpair) + 8 * (lane >> 2);   // of ROWS eights
         const uint32_t rm = (uint32_t)((((lane >> 4) & 1) * 2 + ((lane >> 2) & 1)) * 16 + panel * 8 + quad * 2);
         const uint32_t afull0 = mapa_shared(smem_u32(&afull[0]), 0), sig0 = mapa_shared(smem_u32(signals), 0);
         const uint32_t sig_src = smem_u32(signals + 16 * C::NS * C::GWARPS);
@@ -454,11 +457,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
             // Rows past d_out and stages past the slice come as zeros, which place
             // zeros.
             auto copy = [&](int b, int i) {
-                if (i < it.k1) {
+                if (i < it.k1 && lane < 4 * C::ROWS) {
                     const int64_t k = (int64_t)i * kK + mrow;
                     const bool there = in && k < p.d_out;
                     const uint8_t *src = there ? p.meta + k * mld + d / 8 : p.meta;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(meta0 + b * 512 + lane * 16)),
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(meta0 + b * C::ROWS * 64 + lane * 16)),
                                  "l"(src), "r"(there ? 16 : 0)
                                  : "memory");
                 }
@@ -485,9 +488,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDxThreads, 1)
                 }
                 __syncwarp();
                 uint8_t *a = smem + s * C::STAGE;
-                const uint8_t *raw = smem + C::RAW_OFF + rs * (H * kValBytes), *meta = meta0 + b * 512;
+                const uint8_t *raw = smem + C::RAW_OFF + rs * (H * kValBytes), *meta = meta0 + b * C::ROWS * 64;
 #pragma unroll
-                for (int h = 0; h < kGRows; ++h) {
+                for (int h = 0; h < C::ROWS; ++h) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(raw + rv + h * 1024);
                     const uint32_t m = *reinterpret_cast<const uint16_t *>(meta + rm + h * 64);
                     uint4 lo, hi;
@@ -632,7 +635,7 @@ cudaError_t launch_input_backward(const uint16_t *dY, int64_t M, const uint16_t 
     const int64_t pairs = items < sms / 2 ? items : sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(kDxThreads);
+    cfg.blockDim = dim3(plan.halves == 1 ? DxCfg<1>::THREADS : DxCfg<2>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
