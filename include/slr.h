@@ -409,7 +409,7 @@ SLR_API slr_status slr_forward_ex(const void *X, int64_t M, const void *vals, co
  *         d_out): the residual stream is then updated in place.  Otherwise R
  *         must not overlap an output.
  *   Z     device, bf16 [M, d_out], out, or NULL: the pre-activation, rounded to
- *         bf16, for slr_epilogue_backward.
+ *         bf16, for slr_epilogue_backward.  Not Y or R (SLR_ERR_ARG).
  *
  * With SLR_FWD_OVERLAP_PRECEDING, bias counts as a weight (the preceding
  * kernel must not write it); R is read after the preceding kernel is done.

@@ -517,6 +517,7 @@ slr_status slr_forward_epilogue(const void *X, int64_t M, const void *vals, cons
     if (R != nullptr && M > 1 && ldr % 8 != 0 && slr::resolve(path, M, d_out, d_in) == SLR_PATH_TENSOR)
         return SLR_ERR_SHAPE;
     if (!slr::aligned2(bias) || !slr::aligned16(R) || !slr::aligned16(Z)) return SLR_ERR_ALIGN;
+    if (Z != nullptr && (Z == Y || Z == R)) return SLR_ERR_ARG;   // Z has memory of its own
     slr::Epilogue ep;
     ep.bias = static_cast<const uint16_t *>(bias);
     ep.res = static_cast<const uint16_t *>(R);

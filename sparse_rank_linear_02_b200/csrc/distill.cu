@@ -24,14 +24,16 @@
 // 16-byte boundary, vectors, and a tail.
 //
 // Measured, k = 64, against the copy bandwidth: 4096 x 131072 forward 163 us
-// (1.01), backward 339 (0.97), both in one pass 496 (0.66); 4096 x 32000 49 / 97
-// / 133 us; one token of 131072 6.3 / 6.6 / 8.3 us.  The one pass is short of
-// its 4 bytes a logit because most of its second reads miss L2 again (two thirds
-// by the counters, with a row per SM in flight).  Tried and not kept for it: a
+// (1.01), backward 339 (0.97), both in one pass 440 (0.74); 4096 x 32000 49 / 97
+// / 122 us; one token of 131072 5.9 / 5.2 / 7.9 us.  The one pass is short of its
+// 4 bytes a logit because part of its second reads miss L2 again (two thirds by
+// the counters with a row per SM in flight and no preference; asking L2 to keep
+// the rows until then took 498 us to 440).  Tried and not kept for it: a
 // persistent CTA per SM that keeps a row in shared memory (502 us: its two
 // passes take turns with HBM), the gradient of one row beside the statistics of
-// the next (525 us read from L2, 666 us kept in clusters of two), and clusters
-// that keep the row in registers (610 to 644 us: two cluster barriers a row).
+// the next (525 us read from L2, 666 us kept in clusters of two), clusters that
+// keep the row in registers (610 to 644 us: two cluster barriers a row), and
+// stores that leave L2 first (no gain).
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "tc_ptx.cuh"
@@ -49,6 +51,28 @@ __device__ __forceinline__ uint4 ld_v4(const uint16_t *p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+// The same for a row that is read twice: its lines stay in L2 in preference to
+// others until the second read, which gives them up first.
+__device__ __forceinline__ uint4 ld_keep_v4(const uint16_t *p) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .b64 pol;\n\t"
+        "createpolicy.fractional.L2::evict_last.b64 pol, 1.0;\n\t"
+        "ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], pol;\n\t}"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_last_v4(const uint16_t *p) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .b64 pol;\n\t"
+        "createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
+        "ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], pol;\n\t}"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p));
     return v;
 }
 __device__ __forceinline__ float ld_z(const uint16_t *p) {
@@ -149,14 +173,17 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
     // teacher's entries and their statistics are worked on while they come.
     uint4 x[kNV];
     const bool fits = v1 - v0 <= (int64_t)T * kNV;
-    auto load = [&](int64_t b) {
+    const bool twice = kLoss && kGrad && !fits;
+    auto load = [&](int64_t b, bool again) {
 #pragma unroll
         for (int u = 0; u < kNV; ++u) {
             const int64_t v = b + tid + (int64_t)u * T;
-            x[u] = v < v1 ? ld_v4(z + head + 8 * v) : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
+            const uint16_t *src = z + head + 8 * v;
+            x[u] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
+            if (v < v1) x[u] = again ? ld_last_v4(src) : twice ? ld_keep_v4(src) : ld_v4(src);
         }
     };
-    load(v0);
+    load(v0, false);
     const float zhead = has_head ? ld_z(z + tid) : 0.f, ztail = has_tail ? ld_z(z + tail + tid) : 0.f;
     const float w = kGrad ? __ldg(a.dloss + m) * a.tau : 0.f;
 
@@ -185,7 +212,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
         if (has_head) r.add(zhead, c);
         if (has_tail) r.add(ztail, c);
         for (int64_t b = v0; b < v1; b += (int64_t)T * kNV) {
-            if (b != v0) load(b);
+            if (b != v0) load(b, false);
             uint32_t mx = 0xFF80FF80u;
 #pragma unroll
             for (int u = 0; u < kNV; ++u)
@@ -294,7 +321,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
         };
         auto q1 = [&](float zz) { return ex2(kLoss ? fmaf(zz - ref, fac, -logs) : fmaf(zz, scale, -ref) * fac); };
         for (int64_t b = v0; b < v1; b += (int64_t)T * kNV) {
-            if (b != v0 || (kLoss && !fits)) load(b);
+            if (b != v0 || twice) load(b, twice);
 #pragma unroll
             for (int u = 0; u < kNV; ++u) {
                 const int64_t v = b + tid + (int64_t)u * T;
@@ -343,7 +370,7 @@ cudaError_t launch_t(const DistillArgs &a, unsigned ks, cudaStream_t stream) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ks > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, distill_kernel<T, kLoss, kGrad>, a);
 }
 

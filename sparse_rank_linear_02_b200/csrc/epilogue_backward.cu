@@ -156,7 +156,7 @@ cudaError_t launch_lanes(const uint16_t *dY, const uint16_t *Z, int64_t M, int64
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ks > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, epilogue_backward_kernel<LANES, ACT>, dY, Z, M, d_out, dZ, db);
 }
 

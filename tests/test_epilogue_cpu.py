@@ -72,6 +72,7 @@ def test_forward_epilogue_argument_errors():
     assert _fwd(act=-1) == ARG and _fwd(act=5) == ARG
     assert _fwd(flags=2) == ARG and _fwd(path=9) == ARG
     assert _fwd(ldr=255) == SHAPE
+    assert _fwd(Z=0x6000) == ARG and _fwd(Z=0x9000) == ARG   # the pre-activation in Y's or R's memory
     assert _fwd(R=0x6000, ldr=264) == SHAPE        # Y itself as residual has Y's rows
     assert _fwd(bias=0x8001) == ALIGN and _fwd(R=0x9002) == ALIGN and _fwd(Z=0xa008) == ALIGN
     assert _fwd(ldr=260) == SHAPE                  # the tensor-core path's rows of R are 16-byte aligned
