@@ -47,6 +47,7 @@
 // Every wait is bounded; on expiry an error word is set (slr_check_kernel_error).
 #include <cuda.h>
 
+#include <cstdlib>
 #include <cstring>
 
 #include "tc_gemm.cuh"
@@ -553,13 +554,17 @@ __global__ void __launch_bounds__(256) input_backward_sum_kernel(const float *__
 // (2 n cycles a half) and its bytes at the 35 a cycle that an SM takes in
 // (measured: without its MMAs the kernel is hardly faster); the drain of an
 // accumulator that is not overlapped, and a slice's partial tile and the second
-// kernel, cost extra.
+// kernel, cost extra.  (Against all the plans of ten shapes from 16 to 2048
+// tokens, the choice was the fastest or within 7%.)  SLR_DX_HALVES=1|2 forces the
+// halves; used by the tests.
 DxPlan input_backward_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms) {
     const int64_t ut = (M + 15) / 16, nk = (d_out + kK - 1) / kK, nlr = (r + 63) / 64;
     const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
     DxPlan best{1, 0, 0, 1};
     double best_cost = 0;
+    const char *force = getenv("SLR_DX_HALVES");
     for (int h = 1; h <= 2; ++h) {
+        if (force != nullptr && (force[0] == '1' || force[0] == '2') && h != force[0] - '0') continue;
         const int64_t rows = (d_in + 256 * h - 1) / (256 * h), chu = (h == 1 ? DxCfg<1>::MAXN : DxCfg<2>::MAXN) / 16;
         const int64_t tmin = (ut + chu - 1) / chu;
         for (int64_t tt = tmin; tt <= tmin + 6 && tt <= ut; ++tt) {

@@ -42,11 +42,14 @@ class Problem:
         assert not bad.any(), f"{what} {self.shape}: off at {np.argwhere(bad)[0]}: {got[bad][0]} vs {want[bad][0]}, {bad.sum()} in all"
 
 
+@pytest.mark.parametrize("halves", ["1", "2"])   # tiles of one or two 256-column halves
 @pytest.mark.parametrize("M,d_out,d_in,r", [(1, 8, 128, 0), (1, 64, 128, 8), (5, 72, 256, 0), (16, 256, 256, 64),
                                             (17, 520, 384, 72), (64, 4096, 512, 64), (100, 1032, 640, 136),
                                             (241, 264, 1152, 256), (300, 2056, 896, 16), (500, 136, 4096, 128),
-                                            (1000, 1000, 2048, 8), (33, 14336, 256, 64)])
-def test_input_backward(M, d_out, d_in, r):
+                                            (1000, 1000, 2048, 8), (33, 14336, 256, 64),
+                                            (960, 200, 640, 192), (2100, 328, 1408, 24)])
+def test_input_backward(M, d_out, d_in, r, halves, monkeypatch):
+    monkeypatch.setenv("SLR_DX_HALVES", halves)
     p = Problem(M, d_out, d_in, r, M + d_out + d_in + r)
     dX = slr.input_backward(*p.device())
     torch.cuda.synchronize()
@@ -81,7 +84,9 @@ def test_what_lies_behind_and_empty_batch():
     assert slr.input_backward(ops[0][:0], *ops[1:]).shape == (0, 384)
 
 
-def test_zero_and_nan_rows():
+@pytest.mark.parametrize("halves", ["1", "2"])
+def test_zero_and_nan_rows(halves, monkeypatch):
+    monkeypatch.setenv("SLR_DX_HALVES", halves)
     p = Problem(50, 520, 256, 16, 9)
     dY, vals, meta, U, V = p.device()
     clean = slr.input_backward(dY, vals, meta, U, V)
