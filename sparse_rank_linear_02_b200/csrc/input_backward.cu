@@ -198,6 +198,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DxCfg<H>::THREADS, 1
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_empty + C::NR);
     uint8_t *signals = smem + C::SIG_OFF;
 
+    // The kernel that adds the slices may be scheduled now; it waits for this
+    // grid before it reads a partial tile.
+    asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
