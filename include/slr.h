@@ -21,7 +21,8 @@
  * surface, as usual for CUDA, at the caller's next synchronisation.
  *
  * Threading: calls are safe from several host threads; calls on one stream
- * execute in order.  Outputs must not alias inputs.
+ * execute in order.  Outputs must not alias inputs unless a
+ * call says that they may.
  *
  * Per-device state: on its first use on a device the library looks up, and
  * keeps for the life of the process, the device addresses of its own
@@ -417,6 +418,7 @@ SLR_API slr_status slr_forward_ex(const void *X, int64_t M, const void *vals, co
  * for bit.
  *
  * Accuracy: Z as slr_forward's product; the activation is evaluated in fp32.
+ * At Z = -inf GELU, its tanh form and SILU are NaN (infinity times zero).
  * Requirements: those of slr_forward_ex; bias may have any alignment that its
  * type has (2 bytes), R and Z are 16-byte aligned; on the tensor-core path ldr
  * is a multiple of 8 (M > 1).
@@ -449,8 +451,8 @@ SLR_API slr_status slr_forward_epilogue(const void *X, int64_t M, const void *va
  *   dZ   device, bf16 [M, d_out], out, or NULL.  May be dY or Z itself.
  *   db   device, fp32 [d_out], out, or NULL (not both).
  *
- * relu's slope is 1 for Z > 0, else 0; at infinite Z the slopes of the others
- * are their limits; NaN gives NaN.  The products are fp32 and rounded to bf16
+ * relu's slope is 1 for Z > 0, else 0 (for NaN too); at infinite Z the slopes of
+ * the others are their limits, at NaN they are NaN.  The products are fp32 and rounded to bf16
  * once; db adds them unrounded, in fp32 (a thread's sums of at most 64 rows
  * first), in a fixed order: results are deterministic.
  *
@@ -482,7 +484,9 @@ SLR_API slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t 
  * fp32 accumulation; G is rounded to bf16 between the products (the tensor cores
  * read bf16), dX once.  Deterministic: where the sum over d_out is split, the
  * fp32 partials are added in slice order.  Accuracy (tested): as slr_forward's
- * contract, with B = |dY| |S| + |dY| |U| |V|.
+ * contract, with B = |dY| |S| + |dY| |U| |V|.  The dense operand holds S's zeros:
+ * an infinity or NaN in a token's dY reaches the token's whole row of dX (and no
+ * other row).
  *
  * Requirements: M >= 0 (M == 0 does nothing), d_out >= 8 with d_out % 8 == 0,
  * d_in >= 128 with d_in % 128 == 0, 0 <= r <= 256 with r % 8 == 0, M, d_out, d_in
@@ -513,7 +517,9 @@ SLR_API size_t slr_input_backward_workspace_size(int64_t M, int64_t d_out, int64
  * entries has loss 0, lse 0 and a zero gradient whatever its logits hold; a
  * token with dloss 0 has a zero gradient whatever its logits hold.  A column
  * listed more than once counts with the sum of its p.  A -inf student logit has
- * q = 0 (its listed p makes the loss +inf); NaN and +inf logits give NaN.
+ * q = 0 (its listed p makes the loss +inf); NaN and +inf logits give NaN, and so
+ * does a row of -inf alone.  lse is in units of z / tau: it overflows where the
+ * largest of them does.
  *
  *   logits   device, bf16 [M, ldz] (ldz >= n_vocab).
  *   idx      device, int32 [M, k];   teacher  device, fp32 [M, k].

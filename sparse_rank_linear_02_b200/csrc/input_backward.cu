@@ -36,9 +36,10 @@
 //
 // What bounds it: MMAs and the SM's intake of dY, values and metadata, about
 // equal (34 KB and 960 MMA cycles a stage of two halves x 240 tokens).  Measured,
-// 2048 tokens of 14336 x 4096 without the rank term: 170 us = 1410 TF/s of the
-// dense product (cuBLAS: 1670); all of S by 16-byte loads 186 us; one half 193;
-// eight warps on every stage instead of groups in turn 252.
+// 2048 tokens of 14336 x 4096 without the rank term: 165 us = 1461 TF/s of the
+// dense product (cuBLAS: 1670), 180 with it (r = 64).  Steps on the way there:
+// all of S by 16-byte loads 186 us, one half 193, eight warps on every stage
+// instead of groups in turn 252.
 //
 // Few tiles (short batches): the K stages are split over the pairs that would
 // idle; slices leave fp32 partial tiles in the workspace, which a second kernel

@@ -968,7 +968,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEpi ? kThreads2E : 
             }
             ++it;
         }
-        if (store_thread) bulk_wait_all();
+        if (store_thread) {
+            if (!ok && res) {   // gave up: residual pieces may still be on their way
+                mbar_wait(&rbar[k & 1], (k >> 1) & 1);
+                mbar_wait(&rbar[(k + 1) & 1], ((k + 1) >> 1) & 1);
+            }
+            bulk_wait_all();
+        }
     } else {
         // ------------------------------------------------------------ epilogue (each CTA, its 128 rows)
         const int quarter = warp & 3;
@@ -2891,8 +2897,9 @@ cudaError_t launch_sparse_small(const uint16_t *X, int64_t M, const uint16_t *va
 // plain forward takes it, else the pair kernels with two accumulators, whose
 // epilogue runs beside the next chunk's MMAs.  The 512-row kernel has no room
 // for that (its accumulators are drained between chunks): on the 14336 x 4096
-// layer at 2048 tokens, where the plain forward takes it (121 us against 130),
-// a drain with tanh GELU took 304 us, the 256-row kernel's whole call 149.
+// layer at 2048 tokens, where the plain forward takes it (126 us), a drain with
+// tanh GELU took 304 us, the 256-row kernel's whole call 134 (131 with the bias
+// alone).  777 tokens of 4096 x 14336, r = 128: 74 us plain, 79 to 83 here.
 cudaError_t launch_epilogue(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta, int64_t d_out,
                             int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r, uint16_t *Y, int pdl,
                             const char *force, const Epilogue &ep, cudaStream_t stream) {
