@@ -23,17 +23,23 @@
 // Rows start at any 2-byte boundary: a row is cut into a head up to the first
 // 16-byte boundary, vectors, and a tail.
 //
-// Measured, k = 64, against the copy bandwidth: 4096 x 131072 forward 163 us
-// (1.01), backward 339 (0.97), both in one pass 440 (0.74); 4096 x 32000 49 / 97
-// / 122 us; one token of 131072 5.9 / 5.2 / 7.9 us.  The one pass is short of its
-// 4 bytes a logit because part of its second reads miss L2 again (two thirds by
-// the counters with a row per SM in flight and no preference; asking L2 to keep
-// the rows until then took 498 us to 440).  Tried and not kept for it: a
-// persistent CTA per SM that keeps a row in shared memory (502 us: its two
-// passes take turns with HBM), the gradient of one row beside the statistics of
-// the next (525 us read from L2, 666 us kept in clusters of two), clusters that
-// keep the row in registers (610 to 644 us: two cluster barriers a row), and
-// stores that leave L2 first (no gain).
+// The one pass takes the rounds of its gradient backwards: the last one is still in
+// the registers, and those just before it are the likeliest to be in L2, which is
+// asked to keep a row until its second read.
+//
+// Measured, k = 64, against the copy bandwidth: 4096 x 131072 forward 165 us
+// (1.00), backward 336 (0.98), both in one pass 413 (0.79); 4096 x 32000 49 / 93
+// / 107 us; one token of 131072 5.9 / 5.2 / 7.9 us.  The one pass is short of its
+// 4 bytes a logit by its second reads, from L2 or past it (498 us before L2 was
+// asked to keep rows, 440 forwards; without the first pass's exponentials it is
+// 3% faster).  Tried and not kept for it: part of the row in shared memory (459
+// us, less of it left to L1), the next round's loads
+// among the present one's stores (481 us, and 437 for the backward alone: reads
+// in long bursts suit HBM better), a persistent CTA per SM that keeps a row in
+// shared memory (502 us: its two passes take turns with HBM), the gradient of one
+// row beside the statistics of the next (525 us read from L2, 666 us kept in
+// clusters of two), clusters that keep the row in registers (610 to 644 us: two
+// cluster barriers a row), and stores that leave L2 first (no gain).
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "tc_ptx.cuh"
@@ -41,7 +47,6 @@
 namespace slr {
 namespace {
 
-constexpr int kMaxK = SLR_DISTILL_MAX_K;
 constexpr int kNV = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -146,8 +151,10 @@ struct DistillArgs {
 template <int T, bool kLoss, bool kGrad>
 __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_constant__ DistillArgs a) {
     constexpr int kWarps = T / 32;
-    __shared__ __align__(16) int32_t sh_i[kMaxK];
-    __shared__ float sh_p[kMaxK], sh_z[kMaxK];
+    // The teacher's entries: columns (read four at a time), probabilities, the slice's logits.
+    extern __shared__ __align__(16) int32_t sh_i[];
+    const int k4 = (a.k + 3) & ~3;
+    float *const sh_p = reinterpret_cast<float *>(sh_i + k4), *const sh_z = sh_p + k4;
     __shared__ float row_m[kWarps], row_s[kWarps], tea_m[kWarps], tea_s[kWarps], part_w[kWarps];
     __shared__ float peer_m[8], peer_s[8], peer_l[8];
     uint32_t ks_n;
@@ -172,25 +179,25 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
     // The first vectors are requested before anything is waited for: the
     // teacher's entries and their statistics are worked on while they come.
     uint4 x[kNV];
-    const bool fits = v1 - v0 <= (int64_t)T * kNV;
-    const bool twice = kLoss && kGrad && !fits;
-    auto load = [&](int64_t b, bool again) {
+    constexpr bool kBoth = kLoss && kGrad;
+    const int nb = (int)((v1 - v0 + T * kNV - 1) / (T * kNV));   // rounds of kNV vectors per thread
+    auto load = [&](int i, bool again) {
 #pragma unroll
         for (int u = 0; u < kNV; ++u) {
-            const int64_t v = b + tid + (int64_t)u * T;
+            const int64_t v = v0 + tid + ((int64_t)i * kNV + u) * T;
             const uint16_t *src = z + head + 8 * v;
             x[u] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);   // -inf
-            if (v < v1) x[u] = again ? ld_last_v4(src) : twice ? ld_keep_v4(src) : ld_v4(src);
+            if (v < v1) x[u] = again ? ld_last_v4(src) : kBoth && i < nb - 1 ? ld_keep_v4(src) : ld_v4(src);
         }
     };
-    load(v0, false);
+    load(0, false);
     const float zhead = has_head ? ld_z(z + tid) : 0.f, ztail = has_tail ? ld_z(z + tail + tid) : 0.f;
     const float w = kGrad ? __ldg(a.dloss + m) * a.tau : 0.f;
 
     // Teacher entries, their maximum and sum, and the slice's listed logits.  A
     // NaN logit is kept as the maximum's mark (+inf would give NaN as well).
     MaxSum t{-INFINITY, 0.f};
-    if (tid < 3 && k + tid < kMaxK) sh_i[k + tid] = -1;   // read with the list, four at a time
+    if (tid < k4 - k) sh_i[k + tid] = -1;
     for (int j = tid; j < k; j += T) {
         const int32_t i = __ldg(a.idx + m * k + j);
         const bool there = i >= 0 && i < a.n;
@@ -211,8 +218,8 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
     if constexpr (kLoss) {
         if (has_head) r.add(zhead, c);
         if (has_tail) r.add(ztail, c);
-        for (int64_t b = v0; b < v1; b += (int64_t)T * kNV) {
-            if (b != v0) load(b, false);
+        for (int i = 0; i < nb; ++i) {
+            if (i != 0) load(i, false);
             uint32_t mx = 0xFF80FF80u;
 #pragma unroll
             for (int u = 0; u < kNV; ++u)
@@ -224,8 +231,8 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
             for (int u = 0; u < kNV; ++u) {
                 const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sum = add2(sum, exp2_2(mul2(add2(pack2(bf16lo_to_f32(xw[i]), bf16hi_to_f32(xw[i])), neg), c2)));
+                for (int j = 0; j < 4; ++j)
+                    sum = add2(sum, exp2_2(mul2(add2(pack2(bf16lo_to_f32(xw[j]), bf16hi_to_f32(xw[j])), neg), c2)));
             }
             float s0, s1;
             unpack2(sum, s0, s1);
@@ -320,19 +327,22 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
             return exp2_2(kLoss ? fma2(add2(zz, nref2), fac2, nlogs2) : mul2(fma2(zz, scale2, nref2), fac2));
         };
         auto q1 = [&](float zz) { return ex2(kLoss ? fmaf(zz - ref, fac, -logs) : fmaf(zz, scale, -ref) * fac); };
-        for (int64_t b = v0; b < v1; b += (int64_t)T * kNV) {
-            if (b != v0 || twice) load(b, twice);
+        // After the statistics the last round is in the registers, and the rounds
+        // just before it are the likeliest to be in L2: they go first.
+        for (int s = 0; s < nb; ++s) {
+            const int i = kBoth ? nb - 1 - s : s;
+            if (s != 0) load(i, kBoth);
 #pragma unroll
             for (int u = 0; u < kNV; ++u) {
-                const int64_t v = b + tid + (int64_t)u * T;
+                const int64_t v = v0 + tid + ((int64_t)i * kNV + u) * T;
                 if (v < v1) {
                     const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
                     uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int j = 0; j < 4; ++j) {
                         float g0, g1;
-                        unpack2(mul2(dup2(w), q2(pack2(bf16lo_to_f32(xw[i]), bf16hi_to_f32(xw[i])))), g0, g1);
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(g1), "f"(g0));
+                        unpack2(mul2(dup2(w), q2(pack2(bf16lo_to_f32(xw[j]), bf16hi_to_f32(xw[j])))), g0, g1);
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(g1), "f"(g0));
                     }
                     put8(v, o);
                 }
@@ -363,6 +373,7 @@ cudaError_t launch_t(const DistillArgs &a, unsigned ks, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.M * ks));
     cfg.blockDim = dim3(T);
+    cfg.dynamicSmemBytes = (size_t)((a.k + 3) & ~3) * 12;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -380,18 +391,20 @@ cudaError_t launch_distill(const DistillArgs &a, cudaStream_t stream) {
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t vecs = a.n / 8;   // of eight logits, at most
     if (vecs <= 128 * kNV) return launch_t<128, kLoss, kGrad>(a, 1, stream);
-    // Few rows: as many threads on each as a cluster gives (64 x 131072: 9.5 /
-    // 12.2 / 15.0 us forward / backward / both with 8 x 256, 21.4 / 32.1 / 47.7
-    // with 1 x 128).  Many: small CTAs, eight to an SM, hide each other's
-    // reductions (4096 x 131072 forward: 163 us with 1 x 128, 178 with 1 x 512,
-    // 361 with 4 x 512); a gradient's pass wants slices of at most 32768 logits
-    // (338 us with 4 x 128, 375 with 1 x 128; 1000 x 50001: 40.8 with 2 x 128,
-    // 43.2 with 1 x 128).
+    // Few rows: as many threads on each as a cluster gives (64 x 131072: 9.3 /
+    // 11.0 / 14.0 us forward / backward / both with 8 x 256, 21.4 / 28.6 / 44.2
+    // with 1 x 128).  Many: small CTAs hide each other's reductions (4096 x
+    // 131072 forward: 165 us with 1 x 128, 180 with 1 x 512, 249 with 2 x 512); a
+    // gradient wants fewer rows at a time (L2 holds them between the passes) and
+    // slices of at most 65536 logits (backward / both: 336 / 413 us with 2 x 256,
+    // 356 / 454 with 1 x 256, 374 / 493 with 1 x 128; 4096 x 32000: 93 / 107 with
+    // 1 x 256, 114 / 153 with 2 x 256).
     if (a.M * 8 < 5 * (int64_t)sms && vecs > 8 * 256) return launch_t<256, kLoss, kGrad>(a, 8, stream);
+    constexpr int T = kGrad ? 256 : 128;
     unsigned ks = 1;
-    while (ks < 8 && ((kGrad && a.n > (int64_t)ks * 32768) || (a.M * ks < 5 * (int64_t)sms && vecs > (int64_t)ks * 256)))
+    while (ks < 8 && ((kGrad && a.n > (int64_t)ks * 65536) || (a.M * ks < 5 * (int64_t)sms && vecs > (int64_t)ks * 2 * T)))
         ks *= 2;
-    return launch_t<128, kLoss, kGrad>(a, ks, stream);
+    return launch_t<T, kLoss, kGrad>(a, ks, stream);
 }
 
 }  // namespace
