@@ -472,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DxCfg<H>::THREADS, 1
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            const int first = (int)((uint32_t)(grp - (int)pos) % C::GROUPS), nst = it.k1 - it.k0 + it.lr;
+            const int first = (grp + C::GROUPS - (int)(pos % C::GROUPS)) % C::GROUPS, nst = it.k1 - it.k0 + it.lr;
             int b = 0;
 #pragma unroll
             for (int t = 0; t < kMetaTurns; ++t) copy(t, it.k0 + first + t * C::GROUPS);
@@ -554,13 +554,15 @@ __global__ void __launch_bounds__(256) input_backward_sum_kernel(const float *__
 }  // namespace
 
 // Halves, tokens per tile and K slices for a problem, by the estimated cycles of
-// the busiest pair: rounds of tiles x stages, a stage at the larger of its MMAs
-// (2 n cycles a half) and its bytes at the 35 a cycle that an SM takes in
-// (measured: without its MMAs the kernel is hardly faster); the drain of an
-// accumulator that is not overlapped, and a slice's partial tile and the second
-// kernel, cost extra.  (Against all the plans of ten shapes from 16 to 2048
-// tokens, the choice was the fastest or within 7%.)  SLR_DX_HALVES=1|2 forces the
-// halves; used by the tests.
+// the busiest pair: rounds of tiles x stages, a stage at the largest of its MMAs
+// (1.7 n cycles a half), its bytes at the 38 a cycle that an SM takes in, and the
+// expansion's traffic in shared memory (620 cycles, 1040 for two halves: what
+// bounds batches of up to a hundred tokens); the drains that are not overlapped,
+// and a slice's partial tile and the second kernel, cost extra.
+// The constants are fitted to the times of up to 14 plans for each of 107 problems
+// (1 to 2048 tokens, 520 x 1408 to 8192 x 28672), where the choice is then within
+// 2.1% of the fastest; on 120 drawn at random it is within 5%, and within 11% for
+// ten that take less than 12 us.  SLR_DX_HALVES=1|2 forces the halves; used by the tests.
 DxPlan input_backward_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms) {
     const int64_t ut = (M + 15) / 16, nk = (d_out + kK - 1) / kK, nlr = (r + 63) / 64;
     const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
@@ -573,12 +575,13 @@ DxPlan input_backward_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, in
         const int64_t tmin = (ut + chu - 1) / chu;
         for (int64_t tt = tmin; tt <= tmin + 6 && tt <= ut; ++tt) {
             const int64_t nu = (ut + tt - 1) / tt, ttiles = (ut + nu - 1) / nu;
-            const double n = 16.0 * nu, bytes = (9216.0 * h + 64.0 * n) / 35.0;
-            const double stage = 2.0 * n * h > bytes ? 2.0 * n * h : bytes;
+            const double n = 16.0 * nu, bytes = (9216.0 * h + 64.0 * n) / 38.0;
+            double stage = 1.7 * n * h > bytes ? 1.7 * n * h : bytes;
+            if (stage < (h == 1 ? 620.0 : 1040.0)) stage = h == 1 ? 620.0 : 1040.0;
             for (int64_t ks = 1; ks <= 8 && ks * 4 <= nk + 3; ++ks) {
                 const int64_t rounds = (rows * ttiles * ks + pairs - 1) / pairs;
-                double cost = rounds * (((nk + ks - 1) / ks + nlr) * stage + (h == 1 ? 1500.0 : 1500.0 + 18.0 * n));
-                if (ks > 1) cost += 5000.0 + (double)ks * M * d_in * 8.0 / (pairs * 40.0);
+                double cost = rounds * (((nk + ks - 1) / ks + nlr) * stage + (h == 1 ? 2000.0 : 2000.0 + 22.0 * n)) + n;
+                if (ks > 1) cost += 2750.0 + (double)ks * M * d_in * 8.0 / (pairs * 78.0);
                 if (best.n == 0 || cost < best_cost) {
                     best = DxPlan{h, (int)(16 * nu), (int)ttiles, (int)ks};
                     best_cost = cost;
