@@ -1101,7 +1101,7 @@ struct CfgT {
     static_assert(NS >= 2, "need at least two stages");
     static_assert(MLEAD < MS && MLEAD % 2 == 0, "metadata lead");
     static_assert(SMEM <= 232448, "shared memory budget");
-    static_assert((2 * NS + 3 * MS + 6) * 8 + 8 <= 1024, "barrier area");
+    static_assert((2 * NS + 3 * MS + 8) * 8 + 8 <= 1024, "barrier area");
 };
 
 constexpr int kThreadsT = 384;  // 12 warps
@@ -1120,9 +1120,13 @@ __device__ __forceinline__ bool spin_count_ge(const unsigned int *p, unsigned in
     }
 }
 
-template <int BN>
+// kEpi: bias, activation, residual and the pre-activation's copy, worked on
+// while the accumulators are drained, which the next chunk's MMAs wait for: for
+// long K, where a chunk's main loop is many times its drain.
+template <int BN, bool kEpi = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
-    tc2t_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm) {
+    tc2t_forward_kernel(const __grid_constant__ Maps2 maps, const __grid_constant__ Params2 prm,
+                        const __grid_constant__ std::conditional_t<kEpi, EpiArgs2, NoEpiArgs2> ea) {
     using C = CfgT<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1135,7 +1139,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
     uint64_t *acc_empty = acc_full + 1;
     uint64_t *tp_full = acc_empty + 1;    // projection phase: T partial complete in TMEM
     uint64_t *tp_empty = tp_full + 1;     // projection phase: T partial drained (leader)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tp_empty + 1);
+    uint64_t *rfull = tp_empty + 1;       // kEpi: residual piece landed, [group][2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rfull + 4);
     volatile uint32_t *fail = tmem_slot + 1;
     uint8_t *meta_ring = smem + C::META_OFF;
     uint8_t *dummy = smem + C::DUMMY_OFF;   // MS signal slots + 1 source slot
@@ -1171,6 +1176,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
         mbar_init(acc_empty, 16);
         mbar_init(tp_full, 1);
         mbar_init(tp_empty, 8);
+        if (kEpi)
+            for (int b = 0; b < 4; ++b) mbar_init(&rfull[b], 1);
         *fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -1592,7 +1599,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
         ChunkIter iter(prm, pair, npairs);
         Chunk ch;
         bool part = false;   // the pair's last chunk is a K slice of a tail tile
-        while (!*fail && iter.next(prm.chu, ch)) {
+        if constexpr (kEpi) {
+            // In units of 16 tokens.  The staging buffer is two pieces: residuals
+            // come by TMA into the piece that their outputs then overwrite, one
+            // unit ahead; with a copy of Z the second piece is Z's, and the next
+            // residual waits for the unit's outputs.
+            const Epilogue &ep = ea.ep;
+            constexpr int kPieceBytes = C::OUT_BYTES / 2;
+            uint8_t *pieces = reinterpret_cast<uint8_t *>(out);
+            uint64_t *rbar = rfull + 2 * grp;
+            const bool res = ep.res != nullptr, pre = ep.pre != nullptr;
+            uint32_t k = 0;   // units so far
+            bool ok = true;
+            auto piece = [&](uint32_t kk) { return pieces + (pre ? 0 : kk & 1) * kPieceBytes; };
+            auto load_res = [&](uint32_t kk, int d0, int tok) {
+                mbar_expect_tx(&rbar[kk & 1], kPieceBytes);
+                tma_load_2d(&ea.r16, smem_u32(piece(kk)), &rbar[kk & 1], d0, tok);
+            };
+            while (ok && iter.next(prm.chu, ch)) {
+                if (ch.part) {
+                    part = true;
+                    break;
+                }
+                const int d0 = ch.d0 + grp * 2 * BM + (int)rank * BM;
+                const int nu = ch.n / 16;
+                float bias = 0.f;
+                if (ep.bias != nullptr && d0 + row < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + d0 + row));
+                if (store_thread && res) {
+                    bulk_wait_read0();
+                    load_res(k, d0, ch.tok0);
+                }
+                bool got = *fail == 0 && mbar_wait_cluster(acc_full, (uint32_t)(it & 1));
+                tc_fence_after();
+                const uint32_t acc = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(grp * BN);
+#pragma unroll 1
+                for (int u = 0; u < nu; ++u, ++k) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(acc + (uint32_t)(u * 16), v);
+                    if (u + 1 == nu) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote_relaxed(empty_leader);
+                    }
+                    if (got && res) got = mbar_wait(&rbar[k & 1], (k >> 1) & 1);
+                    if (store_thread) {
+                        bulk_wait_read0();   // the unit before is read: its pieces are free
+                        if (!pre && got && res && u + 1 < nu) load_res(k + 1, d0, ch.tok0 + (u + 1) * 16);
+                    }
+                    ok = named_bar_and(1 + grp, 128, got);
+                    if (!ok) {
+                        *fail = 1;
+                        if (lane == 0) atomicOr(&g_tc_error, 128u);
+                        break;
+                    }
+                    uint16_t *o = reinterpret_cast<uint16_t *>(piece(k)) + row;
+                    uint16_t *zb = reinterpret_cast<uint16_t *>(pieces + kPieceBytes) + row;
+                    float z[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]) + bias;
+                    if (pre) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) zb[j * BM] = f32_to_bf16_bits(z[j]);
+                    }
+                    act_values<16>(z, ep.act);
+                    if (res) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) z[j] += bf16lo_to_f32(o[j * BM]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j * BM] = f32_to_bf16_bits(z[j]);
+                    fence_proxy_async_smem();
+                    named_bar_sync(1 + grp, 128);
+                    if (store_thread) {
+                        const int tq = ch.tok0 + u * 16;
+                        if (pre) tma_store_2d(&ea.z16, smem_u32(zb - row), d0, tq);
+                        tma_store_2d(&maps.y16, smem_u32(o - row), d0, tq);
+                        bulk_commit();
+                        if (pre && res && u + 1 < nu) {
+                            bulk_wait_read0();
+                            load_res(k + 1, d0, tq + 16);
+                        }
+                    }
+                }
+                ++it;
+            }
+            if (store_thread && !ok && res) {   // gave up: residual pieces may still be on their way
+                mbar_wait(&rbar[k & 1], (k >> 1) & 1);
+                mbar_wait(&rbar[(k + 1) & 1], ((k + 1) >> 1) & 1);
+            }
+        }
+        while (!kEpi && !*fail && iter.next(prm.chu, ch)) {
             if (ch.part) {
                 part = true;
                 break;
@@ -1663,6 +1759,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
             const int tt = (int)((e >> 16) - (int64_t)prm.cyc * npairs);
             const int d0 = ch.d0 + grp * 2 * BM + (int)rank * BM;
             const int64_t sub = ((int)rank * 2 + grp) * (BN * BM);
+            if constexpr (kEpi) {
+                // The residual of this warp's rows and the tokens that it will sum, into L2.
+                if (ea.ep.res != nullptr) {
+                    const uint16_t *rp = ea.ep.res + min(d0 + quarter * 32, d_out - 1);
+                    const int nb = ch.n / 4;
+                    for (int t = 4 * ((nb * cq) / cg) + lane; t < 4 * ((nb * (cq + 1)) / cg); t += 32)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(rp + (int64_t)min(ch.tok0 + t, M - 1) * ea.ep.ldr));
+                }
+            }
             bool ok = mbar_wait_cluster(acc_full, (uint32_t)(it & 1));
             if (ok) {
                 tc_fence_after();
@@ -1708,6 +1813,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
 #pragma unroll 1
                 for (int b = b0; b < b1; b += 8) {
                     float4 sum[8];
+                    uint32_t rr[kEpi ? 8 : 1][2];
+                    if constexpr (kEpi) {
+                        if (ea.ep.res != nullptr)
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                if (b + u < b1) load_res_row<4>(ea.ep, ch.tok0 + 4 * (b + u), M, yrow, d_out, rr[u]);
+                    }
 #pragma unroll 1
                     for (int sl = 0; sl < cg; ++sl) {
                         const float *src = first + (int64_t)sl * kKsSlotFloats;
@@ -1731,7 +1843,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsT, 1)
                             }
                         }
                     }
-                    if (yrow < d_out) {
+                    if constexpr (kEpi) {
+                        const Epilogue &ep = ea.ep;
+                        float z[32];
+                        float bias = 0.f;
+                        if (ep.bias != nullptr && yrow < d_out) bias = bf16lo_to_f32(__ldg(ep.bias + yrow));
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            z[4 * u] = sum[u].x + bias;
+                            z[4 * u + 1] = sum[u].y + bias;
+                            z[4 * u + 2] = sum[u].z + bias;
+                            z[4 * u + 3] = sum[u].w + bias;
+                        }
+                        const int tok0 = ch.tok0 + 4 * b;
+                        const int lim = yrow < d_out ? min(M - tok0, 4 * (b1 - b)) : 0;
+                        if (ep.pre != nullptr) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j < lim) ep.pre[(int64_t)(tok0 + j) * d_out + yrow] = f32_to_bf16_bits(z[j]);
+                        }
+                        act_values<32>(z, ep.act);
+                        if (ep.res != nullptr) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                z[j] += (j & 1) ? bf16hi_to_f32(rr[j / 4][j % 4 / 2]) : bf16lo_to_f32(rr[j / 4][j % 4 / 2]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < lim) prm.y[(int64_t)(tok0 + j) * d_out + yrow] = f32_to_bf16_bits(z[j]);
+                    } else if (yrow < d_out) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
                             const int tok = ch.tok0 + 4 * (b + u);
@@ -1940,12 +2080,25 @@ void plan_pairs(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int chu, int 
     *pairs_out = P;
 }
 
+// The epilogue of a call, as the plans see it: 0 none, else 1, + 1 with an
+// activation that costs arithmetic, + 2 with a residual.
+int epi_class(const Epilogue *ep) {
+    if (ep == nullptr) return 0;
+    return 1 + (ep->act == SLR_ACT_NONE || ep->act == SLR_ACT_RELU ? 0 : 1) + (ep->res != nullptr ? 2 : 0);
+}
+
 // Estimated cycles of the slowest pair for a plan: per chunk, its stages at
 // the larger of the MMA time and the operand bytes over the shared-memory fill
 // rate one SM sustains (about 44 B per cycle measured on B200 for these TMA
 // tiles), plus a fixed cost per chunk (the accumulator drain of the 512-row
 // kernel is not overlapped).  Only used to rank plans.
-double plan_cycles(const Params2 &prm, int pairs, int chu, int half_n, int mode) {
+// epi (epi_class): an epilogue prolongs the 512-row kernel's drain, by the
+// 16-token unit, and its share of a split tile, by the token (fitted: 14336 x 4096
+// at 2048 tokens takes 126 us plain, with a residual / GELU 147 / 155 in the
+// 512-row kernel and 135 / 135 in the 256-row one, whose epilogue runs beside the
+// next chunk's MMAs; 4096 x 14336 118 / 120 and 148 / 145; 8192 x 28672 at 1024,
+// K split, 239 / 239 and 366 / 361).
+double plan_cycles(const Params2 &prm, int pairs, int chu, int half_n, int mode, int epi = 0) {
     // mode 0: 256-row tiles, two accumulators; 1: 256-row, one accumulator;
     // 2: 512-row tiles (one accumulator per half).  A K slice of a split tail
     // tile also writes its fp32 partial (256 rows x n tokens per CTA) and
@@ -1965,6 +2118,13 @@ double plan_cycles(const Params2 &prm, int pairs, int chu, int half_n, int mode)
             const double mma = (tall ? 4.0 : 2.0) * ch.n;
             const int nst = ch.k1 - ch.k0 + (ch.lr ? prm.nlr : 0);
             cyc += nst * (mma > bytes / 44.0 ? mma : bytes / 44.0) + overhead;
+            if (tall && epi != 0) {
+                const bool costly = ((epi - 1) & 1) != 0, res = epi > 2;
+                if (ch.part)
+                    cyc += (double)ch.n * nst / (prm.nk + prm.nlr) * (60.0 + (costly ? 50.0 : 0.0) + (res ? 250.0 : 0.0));
+                else
+                    cyc += ch.n / 16 * (1200.0 + (costly ? 500.0 : 0.0) + (res ? 400.0 : 0.0));
+            }
             if (ch.part) cyc += 2.0 * 256 * 4 * ch.n / 32.0;
         }
         if (cyc > worst) worst = cyc;
@@ -1983,14 +2143,13 @@ struct PlanChoice {
     int tail;   // plan_pairs' tail_mode
 };
 
-// epi: only the kinds whose epilogue runs beside the next chunk's MMAs (two
-// accumulators) and has the form with bias, activation and residual.
-PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms, bool allow_ksplit,
-                       bool epi = false) {
+// epi: as plan_cycles; kind 3 has no form with an epilogue.
+PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sms, bool allow_ksplit, int epi = 0) {
     struct Key {
         int64_t M, d_out, d_in, r;
         int sms;
-        bool ks, epi;
+        bool ks;
+        int epi;
     };
     static std::mutex mu;
     static Key keys[64];
@@ -2007,7 +2166,7 @@ PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sm
     PlanChoice best{-1, 0, 1};
     double best_cost = 0;
     for (int kind = 0; kind < 4; ++kind) {
-        if (epi && kind >= 2) continue;
+        if (epi != 0 && kind == 3) continue;
         if (kind == 0 && M >= 192) continue;   // 128-token chunks: below 192 tokens only
         const int cap = kind == 0 ? Cfg2<128>::CHU : kind == 3 ? Cfg2<256>::CHU : Cfg2<240>::CHU;
         const int half_n = cap * 8;
@@ -2018,7 +2177,7 @@ PlanChoice choose_plan(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int sm
                 Params2 plan;
                 int pairs = 0;
                 plan_pairs(M, d_out, d_in, r, chu, kind == 2 ? 4 * BM : 2 * BM, maxp, tm, &plan, &pairs);
-                const double cost = plan_cycles(plan, pairs, chu, half_n, kind == 2 ? 2 : kind == 3 ? 1 : 0);
+                const double cost = plan_cycles(plan, pairs, chu, half_n, kind == 2 ? 2 : kind == 3 ? 1 : 0, epi);
                 if (best.kind < 0 || cost < best_cost) {
                     best = PlanChoice{kind, chu, tm};
                     best_cost = cost;
@@ -2104,6 +2263,15 @@ int64_t plan_check(int64_t M, int64_t d_out, int64_t d_in, int64_t r, int kernel
     return bad;
 }
 
+// The epilogue's operands with the tensor maps of those that are there.
+bool make_epi_args(EpiArgs2 *ea, const Epilogue &ep, int64_t M, int64_t d_out) {
+    memset(ea, 0, sizeof *ea);
+    ea->ep = ep;
+    if (ep.res != nullptr && !make_map(&ea->r16, kBF16, ep.res, d_out, M, ep.ldr * 2, BM, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return false;
+    return ep.pre == nullptr || make_map(&ea->z16, kBF16, ep.pre, d_out, M, d_out * 2, BM, 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 template <int BN, bool kEpi = false>
 cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
@@ -2151,26 +2319,21 @@ cudaError_t launch_sparse_pair(const uint16_t *X, int64_t M, const uint16_t *val
     cfg.numAttrs = (after_projection && r > 0) ? 1 : 0;
     if constexpr (kEpi) {
         EpiArgs2 ea;
-        memset(&ea, 0, sizeof ea);
-        ea.ep = *ep;
-        if (ep->res != nullptr &&
-            !make_map(&ea.r16, kBF16, ep->res, d_out, M, ep->ldr * 2, BM, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
-            return cudaErrorInvalidValue;
-        if (ep->pre != nullptr &&
-            !make_map(&ea.z16, kBF16, ep->pre, d_out, M, d_out * 2, BM, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
-            return cudaErrorInvalidValue;
+        if (!make_epi_args(&ea, *ep, M, d_out)) return cudaErrorInvalidValue;
         return cudaLaunchKernelEx(&cfg, tc2_forward_kernel<BN, true>, maps, prm, ea);
     } else {
         return cudaLaunchKernelEx(&cfg, tc2_forward_kernel<BN, false>, maps, prm, NoEpiArgs2{});
     }
 }
 
-template <int BN>
+template <int BN, bool kEpi = false>
 cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta,
                                int64_t d_out, int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r,
                                uint16_t *Y, bool after_projection, int tail_mode, cudaStream_t stream, int chu = 0,
-                               const uint16_t *V = nullptr, uint8_t *fused_ws = nullptr, size_t ws_bytes = 0) {
+                               const uint16_t *V = nullptr, uint8_t *fused_ws = nullptr, size_t ws_bytes = 0,
+                               const Epilogue *ep = nullptr) {
     using C = CfgT<BN>;
+    const auto kernel = tc2t_forward_kernel<BN, kEpi>;
     // With a fused workspace (single-call forward, r > 0) T lives in its
     // first region; the kernel forms T itself (projection phase) when r <=
     // 128, and the last round may be split along K (partials and counters in
@@ -2194,7 +2357,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t err = cudaFuncSetAttribute(tc2t_forward_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     Params2 prm;
     int pairs = 0;
@@ -2210,7 +2373,7 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
         occ.gridDim = dim3((unsigned)(2 * max_pairs));
         occ.blockDim = dim3(kThreadsT);
         occ.dynamicSmemBytes = C::SMEM;
-        err = cudaOccupancyMaxActiveClusters(&ncl, tc2t_forward_kernel<BN>, &occ);
+        err = cudaOccupancyMaxActiveClusters(&ncl, kernel, &occ);
         if (err != cudaSuccess) return err;
         if (ncl < max_pairs) max_pairs = ncl;
         if (max_pairs < 1) return cudaErrorInvalidConfiguration;
@@ -2280,7 +2443,13 @@ cudaError_t launch_sparse_tall(const uint16_t *X, int64_t M, const uint16_t *val
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (after_projection && r > 0 && !tp) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tc2t_forward_kernel<BN>, maps, prm);
+    if constexpr (kEpi) {
+        EpiArgs2 ea;
+        if (!make_epi_args(&ea, *ep, M, d_out)) return cudaErrorInvalidValue;
+        return cudaLaunchKernelEx(&cfg, kernel, maps, prm, ea);
+    } else {
+        return cudaLaunchKernelEx(&cfg, kernel, maps, prm, NoEpiArgs2{});
+    }
 }
 
 
@@ -2560,10 +2729,14 @@ inline int small_cluster(int64_t work, int64_t stages, int sms) {
 // to M = 512 (32 tiles) 19-22 vs 19-26 us; 4096 x 14336 at M = 65..512 37-64
 // vs 60-67 us (160 tiles at M = 640: 106 vs 73 us, pairs ahead); 8192 x 28672
 // at M = 65..256 72-115 vs 111-131 us; 14336 x 4096 (112 tiles, short K) and
-// 28672 x 8192 (224 tiles) stay on the pair kernels.
-inline bool small_wins(int64_t M, int64_t d_out, int64_t d_in, int sms) {
+// 28672 x 8192 (224 tiles) stay on the pair kernels.  With an epilogue, whose
+// residual and outputs the kernel moves by 2-byte accesses, the tiles have to fit
+// twice: bias and residual on 4096 x 14336 at M = 256 / 384 (64 / 96 tiles) 47 / 75
+// us against 52 / 58, on 2048 x 8192 at M = 512 / 777 (64 / 112) 39 / 50 against
+// 41 / 44.
+inline bool small_wins(int64_t M, int64_t d_out, int64_t d_in, int sms, bool epi = false) {
     const int64_t work = ((d_out + BM - 1) / BM) * ((M + 127) / 128);
-    return work * 4 <= (int64_t)sms || (d_in >= 8192 && work <= (int64_t)sms);
+    return work * 4 <= (int64_t)sms || (d_in >= 8192 && work * (epi ? 2 : 1) <= (int64_t)sms);
 }
 
 template <int BN>
@@ -2894,12 +3067,7 @@ cudaError_t launch_sparse_small(const uint16_t *X, int64_t M, const uint16_t *va
 }
 
 // The forward with bias, activation and residual: the split-K kernel where the
-// plain forward takes it, else the pair kernels with two accumulators, whose
-// epilogue runs beside the next chunk's MMAs.  The 512-row kernel has no room
-// for that (its accumulators are drained between chunks): on the 14336 x 4096
-// layer at 2048 tokens, where the plain forward takes it (126 us), a drain with
-// tanh GELU took 304 us, the 256-row kernel's whole call 134 (131 with the bias
-// alone).  777 tokens of 4096 x 14336, r = 128: 74 us plain, 79 to 83 here.
+// plain forward takes it, else the cheapest plan of the pair kernels.
 cudaError_t launch_epilogue(const uint16_t *X, int64_t M, const uint16_t *vals, const uint8_t *meta, int64_t d_out,
                             int64_t d_in, const uint16_t *U, const uint16_t *T16, int64_t r, uint16_t *Y, int pdl,
                             const char *force, const Epilogue &ep, cudaStream_t stream) {
@@ -2907,10 +3075,14 @@ cudaError_t launch_epilogue(const uint16_t *X, int64_t M, const uint16_t *vals, 
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const bool f128 = force != nullptr && strncmp(force, "2sm128", 6) == 0;
     const bool f240 = force != nullptr && strncmp(force, "2sm240", 6) == 0;
+    const bool ftall = force != nullptr && strncmp(force, "2smtall", 7) == 0;
     const bool fsmall = force != nullptr && strcmp(force, "small") == 0;
-    if (f128 || f240 || (!fsmall && M > kChainMaxM && !small_wins(M, d_out, d_in, sms))) {
-        PlanChoice c = choose_plan(M, d_out, d_in, r, sms, false, true);
-        if (f128 || f240) c = PlanChoice{f128 ? 0 : 1, 0, force[strlen(force) - 1] == 'w' ? 0 : 1};
+    if (f128 || f240 || ftall || (!fsmall && M > kChainMaxM && !small_wins(M, d_out, d_in, sms, true))) {
+        PlanChoice c = choose_plan(M, d_out, d_in, r, sms, false, epi_class(&ep));
+        if (f128 || f240 || ftall) c = PlanChoice{f128 ? 0 : f240 ? 1 : 2, 0, force[strlen(force) - 1] == 'w' ? 0 : 1};
+        if (c.kind == 2)
+            return launch_sparse_tall<240, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl == 1, c.tail, stream,
+                                                 c.chu, nullptr, nullptr, 0, &ep);
         if (c.kind == 0)
             return launch_sparse_pair<128, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, pdl == 1, c.tail, stream,
                                                  c.chu, &ep);
@@ -2997,20 +3169,23 @@ cudaError_t launch_tc_forward_fused(const uint16_t *X, int64_t M, const uint16_t
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const char *force = getenv("SLR_TC_KERNEL");
-    if (r > 0 && ep == nullptr) {
+    if (r > 0) {
         if (force != nullptr) {
             if (strncmp(force, "2smtall", 7) == 0) {
                 const char last = force[strlen(force) - 1];
                 tail = last == 'w' ? 0 : last == 'k' ? 2 : 1;
             }
-        } else if (!tc::small_wins(M, d_out, d_in, sms)) {
-            const tc::PlanChoice c = tc::choose_plan(M, d_out, d_in, r, sms, true);
+        } else if (!tc::small_wins(M, d_out, d_in, sms, ep != nullptr)) {
+            const tc::PlanChoice c = tc::choose_plan(M, d_out, d_in, r, sms, true, tc::epi_class(ep));
             if (c.kind == 2) {
                 tail = c.tail;
                 chu = c.chu;
             }
         }
     }
+    if (tail >= 0 && ep != nullptr)
+        return tc::launch_sparse_tall<240, true>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, false, tail, stream, chu, V,
+                                                 ws, ws_bytes, ep);
     if (tail >= 0)
         return tc::launch_sparse_tall<240>(X, M, vals, meta, d_out, d_in, U, T16, r, Y, false, tail, stream, chu, V,
                                            ws, ws_bytes);

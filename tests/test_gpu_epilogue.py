@@ -105,6 +105,29 @@ def test_epilogue_kernels(kernel, M, d_out, d_in, r, monkeypatch):
     run(Layer(M, d_out, d_in, r, M + r, ldr=d_out + 24), "gelu_tanh", True, True, True, path="tensor")
 
 
+@pytest.mark.parametrize("kernel", ["2smtall", "2smtallw", "2smtallk"])   # last round by tokens, whole, along K
+@pytest.mark.parametrize("M,d_out,d_in,r", [(65, 264, 256, 0), (300, 1032, 512, 64), (777, 520, 1152, 8), (1000, 2056, 512, 136),
+                                            (1200, 8200, 256, 64), (250, 1024, 2048, 128)])
+@pytest.mark.parametrize("act,bias,res,pre", [("none", True, True, False), ("gelu", True, False, True),
+                                              ("silu", False, True, True)])
+def test_epilogue_in_the_512_row_kernel(kernel, M, d_out, d_in, r, act, bias, res, pre, monkeypatch):
+    monkeypatch.setenv("SLR_TC_KERNEL", kernel)
+    L = Layer(M, d_out, d_in, r, M + d_out + r, ldr=d_out + 16)
+    run(L, act, bias, res, pre)
+
+
+@pytest.mark.parametrize("kernel", ["2smtall", "2smtallk"])
+def test_residual_stream_in_place_in_the_512_row_kernel(kernel, monkeypatch):
+    monkeypatch.setenv("SLR_TC_KERNEL", kernel)
+    L = Layer(500, 1032, 512, 64, 31)
+    ops, Y = L.device(), to_dev(L.R)
+    first = slr.forward_epilogue(*ops, bias=to_dev(L.bias), act="gelu_tanh", residual=to_dev(L.R))
+    slr.forward_epilogue(*ops, bias=to_dev(L.bias), act="gelu_tanh", residual=Y, out=Y)
+    slr.check_kernel_error()
+    check(Y, None, L, "gelu_tanh", True, True, "in place")
+    assert torch.equal(Y, first)
+
+
 @pytest.mark.parametrize("M,path", [(1, "decode"), (5, "tensor"), (64, "tensor"), (5, "decode"), (129, "tensor"),
                                     (700, "tensor")])
 def test_residual_stream_in_place(M, path):
