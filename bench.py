@@ -50,7 +50,7 @@ SPARSE_RATIO = 2.0   # nominal 2:4 sparse / dense tensor throughput ratio
 
 # DRAM bytes per launch of the dominant kernel from the committed ncu capture
 # (profiles/); valid only for the kernel source it was taken on.
-NCU_TRAFFIC = {"tc_forward": {"source_sha": "24ec4ad74e883ed0", "bytes_per_launch": 118708480}}
+NCU_TRAFFIC = {"tc_forward": {"source_sha": "93dbba825741bfbc", "bytes_per_launch": 117999104}}
 
 
 def layer_of(cfg, name):

@@ -30,9 +30,10 @@
 // Measured, k = 64, against the copy bandwidth: 4096 x 131072 forward 165 us
 // (1.00), backward 336 (0.98), both in one pass 413 (0.79); 4096 x 32000 49 / 93
 // / 107 us; one token of 131072 5.9 / 5.2 / 7.9 us.  The one pass is short of its
-// 4 bytes a logit by its second reads, from L2 or past it (498 us before L2 was
-// asked to keep rows, 440 forwards; without the first pass's exponentials it is
-// 3% faster).  Tried and not kept for it: part of the row in shared memory (459
+// 4 bytes a logit by its second reads, of which L2 still misses half (by the
+// counters 2.47 GB in all, 0.91 of the copy bandwidth; 498 us before L2 was asked
+// to keep rows, 440 forwards; without the first pass's exponentials it is 3%
+// faster).  Tried and not kept for it: part of the row in shared memory (459
 // us, less of it left to L1), the next round's loads
 // among the present one's stores (481 us, and 437 for the backward alone: reads
 // in long bursts suit HBM better), a persistent CTA per SM that keeps a row in
