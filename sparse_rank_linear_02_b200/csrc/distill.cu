@@ -14,7 +14,10 @@
 // read once and kept from the statistics to the gradient, else it is read again
 // (from L2, where it has just been).  A thread's maximum and sum of
 // exponentials (online, rescaled once per NV vectors) join by shuffles, shared
-// memory and the cluster's distributed shared memory, in a fixed order.  The
+// memory and the cluster's distributed shared memory, in a fixed order.  (The
+// CTAs of a cluster learn from one barrier that all have started, arrived at
+// first and waited for before the first store to a peer, the row's loads in
+// between.)  The
 // gradient's pass writes tau q dloss everywhere; after a block barrier the k
 // listed columns of the slice are written again with their p subtracted.
 // Duplicate columns each find the sum of all their p in list order and write
@@ -161,6 +164,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
     uint32_t ks_n;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ks_n));
     const uint32_t ks_q = tc::cluster_ctarank();
+    if (kLoss && ks_n > 1) tc::cluster_arrive_started();
     const int64_t m = blockIdx.x / ks_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
     const float c = kLog2e / a.tau;
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
         r = MaxSum{lane < kWarps ? row_m[lane] : -INFINITY, lane < kWarps ? row_s[lane] : 0.f};
         warp_join(r, c);
         if (ks_n > 1) {
+            tc::cluster_wait_started();
             if (tid < (int)ks_n) {
                 st_cluster_f32(&peer_m[ks_q], tid, r.m);
                 st_cluster_f32(&peer_s[ks_q], tid, r.s);

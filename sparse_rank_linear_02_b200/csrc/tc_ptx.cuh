@@ -306,6 +306,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
         if (clock64() - t0 > kWaitCycles) return false;
     }
 }
+// The two halves of a cluster barrier that only shows that every CTA of the
+// cluster has started, which must be known before one's shared memory is
+// touched: arrive at the kernel's start, wait before the first remote access
+// (all threads; no memory is ordered).
+__device__ __forceinline__ void cluster_arrive_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_started() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
