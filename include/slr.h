@@ -521,6 +521,11 @@ SLR_API size_t slr_input_backward_workspace_size(int64_t M, int64_t d_out, int64
  * does a row of -inf alone.  lse is in units of z / tau: it overflows where the
  * largest of them does.
  *
+ * The backward takes an lse within +-64 as it is given (q is then within 2e-5 of
+ * its value, relative).  Beyond that fp32 no longer holds lse closely enough, and
+ * the backward forms the row's maximum and sum again from the logits (a second
+ * read): its gradient is then slr_distill_loss_grad's, bit for bit.
+ *
  *   logits   device, bf16 [M, ldz] (ldz >= n_vocab).
  *   idx      device, int32 [M, k];   teacher  device, fp32 [M, k].
  *   loss     device, fp32 [M], out.

@@ -530,7 +530,8 @@ def distill_backward(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Ten
                      dloss: torch.Tensor, *, tau: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of :func:`distill_forward`'s losses with respect to the logits
     (bf16) for the upstream ``dloss`` (fp32 [M]), from the forward's ``lse``
-    (``slr_distill_backward``).  ``out`` may be ``logits`` itself."""
+    (``slr_distill_backward``; where ``|lse|`` exceeds 64 the row's statistics are
+    formed again from its logits).  ``out`` may be ``logits`` itself."""
     device, stream, M, n, k, ldz = _distill_operands(logits, idx, teacher)
     _expect("lse", lse, torch.float32, (M,), device)
     _expect("dloss", dloss, torch.float32, (M,), device)

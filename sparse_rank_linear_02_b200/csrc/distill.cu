@@ -22,6 +22,9 @@
 // listed columns of the slice are written again with their p subtracted.
 // Duplicate columns each find the sum of all their p in list order and write
 // the same bits.
+// The gradient from a given lse takes q = exp(z / tau - lse), except in rows whose
+// lse is too large for fp32 to hold it closely (kMaxLse): those read their logits
+// twice (4096 x 131072, all rows so: 452 us against 336).
 //
 // Rows start at any 2-byte boundary: a row is cut into a head up to the first
 // 16-byte boundary, vectors, and a tail.
@@ -53,6 +56,12 @@ namespace {
 
 constexpr int kNV = 8;
 constexpr float kLn2 = 0.6931471805599453f;
+// The largest |lse| that the gradient alone takes as given.  Its spacing, and the
+// roundings of lse and of 1 / tau, put q off by up to 3 x 2^-24 |lse| relative:
+// 1.2e-5 here, but 0.4% at 2^16.  Beyond it (and for an infinite or NaN lse) the
+// row's maximum and sum are formed again from its logits, as the one pass forms
+// them, to the same bits.
+constexpr float kMaxLse = 64.f;
 
 // Coherent loads: the gradient may overwrite the logits.
 __device__ __forceinline__ uint4 ld_v4(const uint16_t *p) {
@@ -198,6 +207,9 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
     load(0, false);
     const float zhead = has_head ? ld_z(z + tid) : 0.f, ztail = has_tail ? ld_z(z + tail + tid) : 0.f;
     const float w = kGrad ? __ldg(a.dloss + m) * a.tau : 0.f;
+    // Whether the row's statistics are formed here: the same for the whole cluster.
+    const float lse_in = kLoss ? 0.f : __ldg(a.lse_in + m);
+    const bool stats = kLoss || !(fabsf(lse_in) <= kMaxLse);
 
     // Teacher entries, their maximum and sum, and the slice's listed logits.  A
     // NaN logit is kept as the maximum's mark (+inf would give NaN as well).
@@ -220,7 +232,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
 
     // Statistics of the row's slice; kept in registers where it fits.
     MaxSum r{-INFINITY, 0.f};
-    if constexpr (kLoss) {
+    if (stats) {
         if (has_head) r.add(zhead, c);
         if (has_tail) r.add(ztail, c);
         for (int i = 0; i < nb; ++i) {
@@ -266,15 +278,18 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
             for (int i = 0; i < 8; ++i) at[i] = (uint16_t)(o[i / 2] >> (16 * (i & 1)));
         }
     };
-    // log2 q = (z scale - ref) c - logs: with the forward's statistics scale is 1
-    // and ref the row's maximum; from a given lse scale is 1 / tau, ref that lse,
-    // the factor log2(e) and logs 0.
+    // log2 q = (z scale - ref) fac - logs: with the row's statistics scale is 1,
+    // ref the row's maximum and fac c; from a given lse scale is 1 / tau, ref that
+    // lse, fac log2(e) and logs 0.
     float scale = 1.f, ref = 0.f, fac = c, logs = 0.f;
-    if constexpr (kLoss) {
+    if (stats) {
         r = MaxSum{lane < kWarps ? row_m[lane] : -INFINITY, lane < kWarps ? row_s[lane] : 0.f};
         warp_join(r, c);
         if (ks_n > 1) {
-            tc::cluster_wait_started();
+            if constexpr (kLoss)
+                tc::cluster_wait_started();
+            else
+                tc::cluster_sync_all();   // every CTA has started
             if (tid < (int)ks_n) {
                 st_cluster_f32(&peer_m[ks_q], tid, r.m);
                 st_cluster_f32(&peer_s[ks_q], tid, r.s);
@@ -287,7 +302,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
         logs = log2f(r.s);
     } else {
         scale = 1.f / a.tau;
-        ref = __ldg(a.lse_in + m);
+        ref = lse_in;
         fac = kLog2e;
     }
     // The entries' probabilities, and their terms of the loss.
@@ -330,13 +345,13 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const __grid_const
         }
         const f32x2 scale2 = dup2(scale), nref2 = dup2(-ref), fac2 = dup2(fac), nlogs2 = dup2(-logs);
         auto q2 = [&](f32x2 zz) {
-            return exp2_2(kLoss ? fma2(add2(zz, nref2), fac2, nlogs2) : mul2(fma2(zz, scale2, nref2), fac2));
+            return exp2_2(fma2(kLoss ? add2(zz, nref2) : fma2(zz, scale2, nref2), fac2, nlogs2));
         };
-        auto q1 = [&](float zz) { return ex2(kLoss ? fmaf(zz - ref, fac, -logs) : fmaf(zz, scale, -ref) * fac); };
+        auto q1 = [&](float zz) { return ex2(fmaf(kLoss ? zz - ref : fmaf(zz, scale, -ref), fac, -logs)); };
         // After the statistics the last round is in the registers, and the rounds
         // just before it are the likeliest to be in L2: they go first.
         for (int s = 0; s < nb; ++s) {
-            const int i = kBoth ? nb - 1 - s : s;
+            const int i = stats ? nb - 1 - s : s;
             if (s != 0) load(i, kBoth);
 #pragma unroll
             for (int u = 0; u < kNV; ++u) {
