@@ -89,12 +89,12 @@ slr_path resolve(slr_path path, int64_t M, int64_t d_out, int64_t d_in) {
     return (M <= kDecodeMaxM && d_out * d_in <= kDecodeMaxWeights) ? SLR_PATH_DECODE : SLR_PATH_TENSOR;
 }
 
-// Host-side validation shared by the forward entry points.  `need_factors`
-// selects which low-rank operands the stage reads.
+// Host-side validation shared by the forward entry points.  `need_U` and `need_V`
+// select which low-rank operands the stage reads; ep: the epilogue's, or null.
 slr_status validate(const void *X, int64_t M, const void *vals, const void *meta, int64_t d_out, int64_t d_in,
                     const void *U, const void *V, int64_t r, const void *Y, const void *workspace,
                     size_t workspace_bytes, slr_path path, bool need_sparse, bool need_U, bool need_V,
-                    slr_path *resolved) {
+                    slr_path *resolved, const Epilogue *ep = nullptr) {
     if (path != SLR_PATH_AUTO && path != SLR_PATH_DECODE && path != SLR_PATH_TENSOR) return SLR_ERR_ARG;
     if (M < 0 || d_out < 0 || d_in < 0 || r < 0) return SLR_ERR_SHAPE;
     const slr_path p = resolve(path, M, d_out, d_in);
@@ -105,10 +105,19 @@ slr_status validate(const void *X, int64_t M, const void *vals, const void *meta
     if (need_sparse && (vals == nullptr || meta == nullptr || Y == nullptr)) return SLR_ERR_NULL;
     if (r > 0 && ((need_U && U == nullptr) || (need_V && V == nullptr))) return SLR_ERR_NULL;
     if (need > 0 && workspace == nullptr) return SLR_ERR_NULL;
+    const uint16_t *R = ep != nullptr ? ep->res : nullptr;
+    const uint16_t *Z = ep != nullptr ? ep->pre : nullptr;
+    if (Z != nullptr && (Z == Y || Z == R)) return SLR_ERR_ARG;   // Z has memory of its own
     if (d_out < 1 || d_in < 128 || d_in % 128 != 0 || r % 8 != 0) return SLR_ERR_SHAPE;
     if (p == SLR_PATH_TENSOR && !tensor_ok(d_out)) return SLR_ERR_SHAPE;
     if (M > INT32_MAX || d_out > INT32_MAX || d_in > INT32_MAX) return SLR_ERR_SHAPE;
+    if (R != nullptr) {
+        if (ep->ldr < d_out || (R == Y && ep->ldr != d_out)) return SLR_ERR_SHAPE;
+        // The tensor-core path loads R by TMA, whose row pitch is a multiple of 16 bytes.
+        if (M > 1 && ep->ldr % 8 != 0 && p == SLR_PATH_TENSOR) return SLR_ERR_SHAPE;
+    }
     if (!aligned16(X)) return SLR_ERR_ALIGN;
+    if (!aligned16(R) || !aligned16(Z) || (ep != nullptr && !aligned2(ep->bias))) return SLR_ERR_ALIGN;
     if (need_sparse && (!aligned16(vals) || !aligned16(meta) || !aligned16(Y))) return SLR_ERR_ALIGN;
     if (r > 0 && ((need_U && !aligned16(U)) || (need_V && !aligned16(V)))) return SLR_ERR_ALIGN;
     if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0) return SLR_ERR_ALIGN;
@@ -176,8 +185,10 @@ slr_status forward_impl(const void *X, int64_t M, const void *vals, const void *
     slr_path p;
     if ((flags & ~(uint32_t)SLR_FWD_OVERLAP_PRECEDING) != 0) return SLR_ERR_ARG;
     const slr_status st = validate(X, M, vals, meta, d_out, d_in, U, V, r, Y, workspace, workspace_bytes, path,
-                                   true, true, true, &p);
+                                   true, true, true, &p, ep);
     if (st != SLR_OK || M == 0) return st;
+    if (ep != nullptr && ep->bias == nullptr && ep->res == nullptr && ep->pre == nullptr && ep->act == SLR_ACT_NONE)
+        ep = nullptr;   // the product itself
     const bool chained = (flags & SLR_FWD_OVERLAP_PRECEDING) != 0 && chain_supported(p, M, d_in, r);
     cudaError_t err = cudaSuccess;
     if (p == SLR_PATH_TENSOR && M > kChainMaxM) {
@@ -512,21 +523,14 @@ slr_status slr_forward_epilogue(const void *X, int64_t M, const void *vals, cons
                                 const void *R, int64_t ldr, void *Z, void *Y, void *workspace, size_t workspace_bytes,
                                 slr_path path, uint32_t flags, slr_stream_t stream) {
     if (!slr::act_ok(act)) return SLR_ERR_ARG;
-    if (R != nullptr && (ldr < d_out || (R == Y && ldr != d_out))) return SLR_ERR_SHAPE;
-    // The tensor-core path loads R by TMA, whose row pitch is a multiple of 16 bytes.
-    if (R != nullptr && M > 1 && ldr % 8 != 0 && slr::resolve(path, M, d_out, d_in) == SLR_PATH_TENSOR)
-        return SLR_ERR_SHAPE;
-    if (!slr::aligned2(bias) || !slr::aligned16(R) || !slr::aligned16(Z)) return SLR_ERR_ALIGN;
-    if (Z != nullptr && (Z == Y || Z == R)) return SLR_ERR_ARG;   // Z has memory of its own
     slr::Epilogue ep;
     ep.bias = static_cast<const uint16_t *>(bias);
     ep.res = static_cast<const uint16_t *>(R);
     ep.ldr = ldr;
     ep.pre = static_cast<uint16_t *>(Z);
     ep.act = (int32_t)act;
-    const bool plain = bias == nullptr && R == nullptr && Z == nullptr && act == SLR_ACT_NONE;
     return slr::forward_impl(X, M, vals, meta, d_out, d_in, U, V, r, Y, workspace, workspace_bytes, path, flags,
-                             reinterpret_cast<cudaStream_t>(stream), plain ? nullptr : &ep);
+                             reinterpret_cast<cudaStream_t>(stream), &ep);
 }
 
 slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t M, int64_t d_out, slr_act act, void *dZ,
