@@ -539,6 +539,7 @@ slr_status slr_epilogue_backward(const void *dY, const void *Z, int64_t M, int64
     if (dZ == nullptr && db == nullptr) return SLR_ERR_NULL;
     if (M > 0 && (dY == nullptr || (act != SLR_ACT_NONE && Z == nullptr))) return SLR_ERR_NULL;
     if (M < 0 || d_out < 8 || d_out % 8 != 0 || M > INT32_MAX || d_out > INT32_MAX) return SLR_ERR_SHAPE;
+    if (act == SLR_ACT_NONE) Z = nullptr;   // not looked at
     if (!slr::aligned16(dY) || !slr::aligned16(Z) || !slr::aligned16(dZ) || !slr::aligned16(db)) return SLR_ERR_ALIGN;
     const slr_status dev = slr::check_device();
     if (dev != SLR_OK) return dev;

@@ -1,11 +1,16 @@
 """Argument checks of the epilogue's entry points: an empty batch looks at no
 pointer, nulls come before sizes and sizes before alignment, and an operand that
 is not looked at is not checked."""
-import pytest
+import ctypes
 
+import pytest
+import torch
+
+import sparse_rank_linear_02_b200 as slr
 from test_epilogue_cpu import _fwd
 
 OK, NULL, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA, TIMEOUT, ARG = range(9)
+P = ctypes.c_void_p
 
 
 @pytest.mark.parametrize("kw", [dict(R=0x9002), dict(Z=0xa008), dict(bias=0x8001), dict(Z=0x6000), dict(Z=0x9000),
@@ -27,3 +32,11 @@ def test_forward_epilogue_checks_in_order():
     assert _fwd(bias=0x8001, ws_bytes=16) == ALIGN
     assert _fwd(Z=0x6000, ldr=255) == ARG and _fwd(Z=0x9000, ws_bytes=16) == ARG   # arguments that never go together
     assert _fwd(ws_bytes=16) == WORKSPACE
+
+
+def test_epilogue_backward_without_an_activation_does_not_look_at_z():
+    f = slr.lib().slr_epilogue_backward
+    dy, dz, db = (P(0x10000 * k) for k in (1, 3, 4))
+    if not torch.cuda.is_available():
+        assert f(dy, P(0x20002), 8, 16, 0, dz, db, None) == DEVICE
+    assert f(dy, P(0x20002), 8, 16, 1, dz, db, None) == ALIGN
