@@ -374,14 +374,8 @@ cudaError_t orthonormalise(float *Q, float *tmp, float *M, float *part, int64_t 
 
 // Device address of g_am_error on the current device.
 unsigned int *am_err() {
-    static unsigned int *addr[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    if (addr[dev] == nullptr) {
-        void *q = nullptr;
-        if (cudaGetSymbolAddress(&q, g_am_error) == cudaSuccess) addr[dev] = static_cast<unsigned int *>(q);
-    }
-    return addr[dev];
+    static std::atomic<unsigned int *> at[kMaxCachedDevices] = {};
+    return device_address(g_am_error, at);
 }
 
 // C (rows x r, fp32) = Z B (B: d_in x r) or Z^T B (B: d_out x r) on the tensor

@@ -5,9 +5,26 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "slr.h"
 
 namespace slr {
+
+// Address of a file-scope device variable on the current device, looked up once
+// per device and kept in `at`; null when there is none.  Host threads may ask at
+// the same time: they find the same address.
+constexpr int kMaxCachedDevices = 64;
+template <typename T>
+T *device_address(const T &symbol, std::atomic<T *> (&at)[kMaxCachedDevices]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return nullptr;
+    if (at[dev] == nullptr) {
+        void *q = nullptr;
+        if (cudaGetSymbolAddress(&q, symbol) == cudaSuccess) at[dev] = static_cast<T *>(q);
+    }
+    return at[dev];
+}
 
 // bf16 bit pattern (low 16 bits of x) -> fp32, exact.
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t x) { return __uint_as_float(x << 16); }

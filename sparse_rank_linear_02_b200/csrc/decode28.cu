@@ -408,14 +408,15 @@ cudaError_t launch28(const uint16_t *X, int64_t M, const uint16_t *vals8, const 
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     // Resident CTAs per SM, asked once per instantiation (a property of the
     // compiled kernel and the sm_100 architecture, the same on every B200).
-    static int per_sm = 0;
+    static std::atomic<int> per_sm_known{0};
+    int per_sm = per_sm_known;
     if (per_sm == 0) {
         int n = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode28_forward_kernel<MT, RW>, kWarps28 * 32, 0) !=
                 cudaSuccess ||
             n < 1)
             n = 1;
-        per_sm = n;
+        per_sm_known = per_sm = n;
     }
     // Row groups of RW rows, one per warp: as many warps as there are groups,
     // up to the resident capacity; with more groups, the fewest whole rounds

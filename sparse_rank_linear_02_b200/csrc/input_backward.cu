@@ -61,14 +61,8 @@ __device__ unsigned int g_dx_error = 0;
 namespace {
 
 unsigned int *dx_err() {
-    static unsigned int *addr[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    if (addr[dev] == nullptr) {
-        void *q = nullptr;
-        if (cudaGetSymbolAddress(&q, g_dx_error) == cudaSuccess) addr[dev] = static_cast<unsigned int *>(q);
-    }
-    return addr[dev];
+    static std::atomic<unsigned int *> at[kMaxCachedDevices] = {};
+    return device_address(g_dx_error, at);
 }
 
 constexpr int kCols = 128;                    // input columns per CTA and half

@@ -31,14 +31,8 @@ namespace {
 
 // Device address of this file's error word on the current device.
 unsigned int *bwd_err() {
-    static unsigned int *addr[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    if (addr[dev] == nullptr) {
-        void *q = nullptr;
-        if (cudaGetSymbolAddress(&q, g_bwd_error) == cudaSuccess) addr[dev] = static_cast<unsigned int *>(q);
-    }
-    return addr[dev];
+    static std::atomic<unsigned int *> at[kMaxCachedDevices] = {};
+    return device_address(g_bwd_error, at);
 }
 
 // A second stream per device, so that dU (which needs only dY and T) runs
