@@ -547,7 +547,7 @@ def distill_backward(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Ten
 def distill_loss_grad(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, dloss: torch.Tensor, *,
                       tau: float = 1.0, out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """``(loss, dlogits)`` of :func:`distill_forward` and :func:`distill_backward`
-    in one pass over the logits, for weights ``dloss`` known beforehand
+    in one call, for weights ``dloss`` known beforehand
     (``slr_distill_loss_grad``).  ``out`` may be ``logits`` itself."""
     device, stream, M, n, k, ldz = _distill_operands(logits, idx, teacher)
     _expect("dloss", dloss, torch.float32, (M,), device)

@@ -8,7 +8,7 @@
 //     dloss_m dL/dz_v = dloss_m tau (q_v - sum of p_j with i_j = v)
 // A token without entries has loss 0 and a zero gradient whatever its logits.
 //
-// Bound by HBM: 2 bytes per logit forward, 4 backward, 4 for both in one pass.
+// Bound by HBM: 2 bytes per logit forward, 4 backward, at least 4 for both in one call.
 // A cluster of KS CTAs owns a row, each a slice of its columns.  A thread holds
 // NV vectors of eight logits; where the slice fits the CTA's registers it is
 // read once and kept from the statistics to the gradient, else it is read again
@@ -29,17 +29,19 @@
 // Rows start at any 2-byte boundary: a row is cut into a head up to the first
 // 16-byte boundary, vectors, and a tail.
 //
-// The one pass takes the rounds of its gradient backwards: the last one is still in
+// The one call takes the rounds of its gradient backwards: the last one is still in
 // the registers, and those just before it are the likeliest to be in L2, which is
 // asked to keep a row until its second read.
 //
-// Measured, k = 64, against the copy bandwidth: 4096 x 131072 forward 165 us
-// (1.00), backward 336 (0.98), both in one pass 413 (0.79); 4096 x 32000 49 / 93
-// / 107 us; one token of 131072 5.9 / 5.2 / 7.9 us.  The one pass is short of its
-// 4 bytes a logit by its second reads, of which L2 still misses half (by the
-// counters 2.47 GB in all, 0.91 of the copy bandwidth; 498 us before L2 was asked
-// to keep rows, 440 forwards; without the first pass's exponentials it is 3%
-// faster).  Tried and not kept for it: part of the row in shared memory (459
+// Measured (a graph of 6 to 96 calls), k = 64, against the copy bandwidth: 4096 x
+// 131072 forward 162 us (1.01), backward 336 (0.98), both in one call 413 (0.79);
+// 4096 x 32000 49 / 92 / 108 us (0.82 / 0.87 / 0.74); one token of 131072 4.8 / 4.2
+// / 6.8 us; 1000 x 50001, k = 20, 23 / 40 / 49 us (0.66 / 0.77 / 0.63: 1000 rows of
+// one CTA fill 592 resident ones 1.7 times).  The one call is above its
+// 4 bytes a logit by its second reads (three quarters of a row of 131072), of which
+// L2 still misses half: by the counters 2.47 GB in all, 4.6 bytes a logit, at 0.91 of
+// the copy bandwidth (498 us before L2 was asked to keep rows, 440 forwards; without
+// the first pass's exponentials it is 3% faster).  Tried and not kept for it: part of the row in shared memory (459
 // us, less of it left to L1), the next round's loads
 // among the present one's stores (481 us, and 437 for the backward alone: reads
 // in long bursts suit HBM better), a persistent CTA per SM that keeps a row in

@@ -5,7 +5,7 @@
 // for Y = act(Z) + R, Z = X S^T + T U^T + b: one pass over dY and Z.  The sums
 // take the fp32 products before their rounding to bf16.
 //
-// Bound by HBM: 6 bytes per element.  A cluster of KS <= 8 CTAs owns a strip of
+// It cannot do with less than 6 bytes of HBM traffic per element.  A cluster of KS <= 8 CTAs owns a strip of
 // 8 * LANES columns and splits its tokens, so one launch also finishes db: the
 // CTAs' column sums meet through distributed shared memory and are added in
 // CTA order (the result does not depend on timing).  LANES threads read a row
@@ -15,8 +15,13 @@
 // (at most 64 rows, then the sums of those), which bounds the rounding for long
 // batches.
 //
-// Measured (176 MB, 27 us at the copy bandwidth): relu 32.8 us, tanh GELU 36.5,
-// GELU 40.0; 2048 x 4096 (50 MB) 12.8 / 13.8 / 14.4; 17 x 4096 3.2.
+// Measured (176 MB, 27 us at the copy bandwidth): relu 33.1 us, SiLU 35.4, tanh GELU
+// 36.8, GELU 40.5; 2048 x 4096 (50 MB) 12.4 / 13.2 / 13.6 / 13.9; 17 x 4096 2.4 to 3.1.
+//
+// What bounds it: the loads of a pass wait until the pass before is computed and
+// stored, so neither memory nor any pipe is busy all the time (GELU: DRAM 36%, special
+// functions 39%, ALU 29%, issue slots 49%; relu: DRAM 55%, ALU 36%, issue slots 34%,
+// and a warp that waits for its loads in most cycles).
 #include "common.cuh"
 #include "epilogue.cuh"
 #include "tc_ptx.cuh"
@@ -163,9 +168,11 @@ cudaError_t launch_lanes(const uint16_t *dY, const uint16_t *Z, int64_t M, int64
 template <int ACT>
 cudaError_t launch_act(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t d_out, uint16_t *dZ, float *db,
                        cudaStream_t stream) {
-    // The widest strip (the longest runs of a row) whose clusters still put two
-    // and a half CTAs on every SM: 2048 x 14336 takes 36.5 / 39.6 / 45.2 us with
-    // 32 / 16 / 8 lanes, 2048 x 4096 23.9 / 17.2 / 13.8.
+    // The widest strip (the longest runs of a row) with which clusters of eight put
+    // two and a half CTAs on every SM: 2048 x 14336 takes 36.5 / 39.6 / 45.2 us with
+    // 32 / 16 / 8 lanes, 2048 x 4096 23.9 / 17.2 / 13.8.  Batches of up to 64, 128 or
+    // 256 tokens (by width) have smaller clusters and fewer CTAs: 16 x 14336 runs 56
+    // of them in 2.8 us, 64 x 14336 224 in 4.7.
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t eighths = (d_out + 63) / 64 * 8;   // CTAs with 8 lanes, eight to a cluster

@@ -34,9 +34,13 @@
 // copies that complete on its barrier, since a release-ordered remote arrive
 // would stall them for most of a microsecond each.
 //
-// What bounds it: MMAs and the SM's intake of dY, values and metadata, about
-// equal (34 KB and 960 MMA cycles a stage of two halves x 240 tokens).  Measured,
-// 2048 tokens of 14336 x 4096 without the rank term: 165 us = 1461 TF/s of the
+// What bounds it: a stage of two halves takes about 1040 cycles whatever its tokens,
+// for the expansion (reads, permutes and writes of shared memory); of one half, 620.
+// Its MMAs take 2 n cycles a half, its 34 KB of dY, values and metadata (240 tokens)
+// 890.  So at 240 tokens the tensor pipe is the bound beside it (87.5% active for
+// 2048 tokens of 14336 x 4096), at 160 the expansion (55% active, the ALU pipe 60%,
+// shared memory 45%, for 777 tokens of 4096 x 14336, 96 us), at 64 the expansion and
+// the three launches (10% active, 64 tokens of 4096 x 4096, 15 us).  Measured, 2048 tokens of 14336 x 4096 without the rank term: 165 us = 1461 TF/s of the
 // dense product (cuBLAS: 1670), 180 with it (r = 64).  Steps on the way there:
 // all of S by 16-byte loads 186 us, one half 193, eight warps on every stage
 // instead of groups in turn 252.
@@ -549,10 +553,11 @@ __global__ void __launch_bounds__(256) input_backward_sum_kernel(const float *__
 
 // Halves, tokens per tile and K slices for a problem, by the estimated cycles of
 // the busiest pair: rounds of tiles x stages, a stage at the largest of its MMAs
-// (1.7 n cycles a half), its bytes at the 38 a cycle that an SM takes in, and the
-// expansion's traffic in shared memory (620 cycles, 1040 for two halves: what
-// bounds batches of up to a hundred tokens); the drains that are not overlapped,
-// and a slice's partial tile and the second kernel, cost extra.
+// (1.7 n cycles a half as fitted, 2 n by the pipe's rate), its bytes at the 38 a cycle
+// that an SM takes in, and the expansion (620 cycles, 1040 for two halves: the
+// largest of the three up to 224 tokens for one half, and always for two); the drains
+// that are not overlapped, and a slice's partial tile and the second kernel, cost
+// extra.
 // The constants are fitted to the times of up to 14 plans for each of 107 problems
 // (1 to 2048 tokens, 520 x 1408 to 8192 x 28672), where the choice is then within
 // 2.1% of the fastest; on 120 drawn at random it is within 5%, and within 11% for
